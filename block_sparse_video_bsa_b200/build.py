@@ -18,8 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsa.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "pool_summarize.cu", "select.cu", "attend.cu", "attend_fp8.cu", "quant_fp8.cu",
-           "reblock.cu", "extra.cu",
-           "noalloc.cu"]
+           "reblock.cu", "extra.cu", "noalloc.cu", "api_block.cu", "rotary.cu", "gate_norm.cu",
+           "quant_int8.cu", "linear_int8.cu"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",

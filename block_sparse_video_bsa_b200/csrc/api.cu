@@ -5,38 +5,11 @@
 #include <cmath>
 #include <mutex>
 
+#include "api_util.h"
 #include "bsa.h"
 #include "bsa_kernels.h"
 
-namespace {
-
-using bsa::Shape;
-
-constexpr int kMaxN = 1 << 21;       // nb <= 16384 (bitmap / score tile sizes)
-constexpr int kMaxBH = 65535;        // grid.y limit of the per-block kernels
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int shape_of(const bsa_params* p, Shape* s) {
-  if (!p) return BSA_ERR_INVALID;
-  if (p->D != 128 || p->B < 1 || p->H < 1 || p->N < 1 || p->N > kMaxN) return BSA_ERR_INVALID;
-  if (static_cast<int64_t>(p->B) * p->H > kMaxBH) return BSA_ERR_INVALID;
-  if (p->top_k < 1) return BSA_ERR_INVALID;
-  if (p->prefix < 0 || p->prefix % 128 != 0 || p->prefix >= p->N) return BSA_ERR_INVALID;
-  if (p->variant != BSA_SUMMARY_ANCHOR && p->variant != BSA_SUMMARY_MEAN) return BSA_ERR_INVALID;
-  s->B = p->B;
-  s->H = p->H;
-  s->N = p->N;
-  s->nb = (p->N + 127) / 128;
-  s->pb = p->prefix / 128;
-  s->nbv = s->nb - s->pb;
-  s->k_eff = p->top_k < s->nbv ? p->top_k : s->nbv;
-  s->kcap = p->prefix > 0 ? s->nb : s->pb + s->k_eff;
-  s->variant = p->variant;
-  s->prefix = p->prefix;
-  s->dev_status = p->dev_status;
-  return BSA_OK;
-}
+namespace bsa {
 
 // The kernels use tcgen05 / TMA: sm_100 only.  Cached per device.
 int check_device() {
@@ -60,11 +33,6 @@ int check_device() {
   return ok[dev] ? BSA_OK : BSA_ERR_UNSUPPORTED;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
@@ -77,6 +45,44 @@ EncodeTiledFn encode_fn() {
       fn = reinterpret_cast<EncodeTiledFn>(ptr);
   });
   return fn;
+}
+
+int cuda_status(cudaError_t e) { return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA; }
+
+}  // namespace bsa
+
+namespace {
+
+using bsa::aligned;
+using bsa::check_device;
+using bsa::cuda_status;
+using bsa::encode_fn;
+using bsa::EncodeTiledFn;
+using bsa::round256;
+using bsa::Shape;
+
+constexpr int kMaxN = 1 << 21;       // nb <= 16384 (bitmap / score tile sizes)
+constexpr int kMaxBH = 65535;        // grid.y limit of the per-block kernels
+
+int shape_of(const bsa_params* p, Shape* s) {
+  if (!p) return BSA_ERR_INVALID;
+  if (p->D != 128 || p->B < 1 || p->H < 1 || p->N < 1 || p->N > kMaxN) return BSA_ERR_INVALID;
+  if (static_cast<int64_t>(p->B) * p->H > kMaxBH) return BSA_ERR_INVALID;
+  if (p->top_k < 1) return BSA_ERR_INVALID;
+  if (p->prefix < 0 || p->prefix % 128 != 0 || p->prefix >= p->N) return BSA_ERR_INVALID;
+  if (p->variant != BSA_SUMMARY_ANCHOR && p->variant != BSA_SUMMARY_MEAN) return BSA_ERR_INVALID;
+  s->B = p->B;
+  s->H = p->H;
+  s->N = p->N;
+  s->nb = (p->N + 127) / 128;
+  s->pb = p->prefix / 128;
+  s->nbv = s->nb - s->pb;
+  s->k_eff = p->top_k < s->nbv ? p->top_k : s->nbv;
+  s->kcap = p->prefix > 0 ? s->nb : s->pb + s->k_eff;
+  s->variant = p->variant;
+  s->prefix = p->prefix;
+  s->dev_status = p->dev_status;
+  return BSA_OK;
 }
 
 // bf16 [BH, rows, 128] viewed as a 3-D tensor; box = 64 columns (128 bytes,
@@ -153,8 +159,6 @@ const bsa::SelectMaps* select_maps(const Shape& s, const float* qpool, const flo
     return nullptr;
   return m;
 }
-
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // The FP8 operand set carved from one buffer in the order of
 // bsa_fp8_operands (each piece 256-byte aligned); returns the bytes used.
@@ -248,8 +252,6 @@ size_t carve(const Shape& s, uint8_t* base, Workspace* w) {
   }
   return off;
 }
-
-int cuda_status(cudaError_t e) { return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA; }
 
 int pool_impl(const Shape& s, const void* Q, float* qpool, float* anchor, cudaStream_t st) {
   return cuda_status(bsa::launch_pool(s, Q, qpool, anchor, st));

@@ -1,0 +1,355 @@
+// C ABI of the operators around the attention (declared in include/bsa.h):
+// argument checks, tensor maps and launches.  No memory is allocated and no
+// state kept.
+#include <cmath>
+
+#include "api_util.h"
+#include "bsa.h"
+#include "bsa_kernels.h"
+
+namespace {
+
+using bsa::aligned;
+using bsa::check_device;
+using bsa::cuda_status;
+
+constexpr int kMaxN = 1 << 21;        // tokens a batch entry, as the attention
+constexpr int kMaxGrid = 65535;
+constexpr int kMaxRow = 32768;        // values of a normed or quantised row; K of the product
+
+int type_size(int t) { return t == BSA_DTYPE_BF16 ? 2 : (t == BSA_DTYPE_FP32 ? 4 : 1); }
+bool float_type(int t) { return t == BSA_DTYPE_BF16 || t == BSA_DTYPE_FP32; }
+
+// Bytes [lo, hi) that rows of `row` values reach from base.
+struct Range {
+  uintptr_t lo, hi;
+};
+Range range_of(const void* base, int size, int64_t row, int64_t n0, int64_t s0, int64_t n1 = 1,
+               int64_t s1 = 0, int64_t n2 = 1, int64_t s2 = 0) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
+  const unsigned __int128 hi =
+      lo + (static_cast<unsigned __int128>(n0 - 1) * s0 + static_cast<unsigned __int128>(n1 - 1) * s1 +
+            static_cast<unsigned __int128>(n2 - 1) * s2 + row) * size;
+  return Range{lo, hi > UINTPTR_MAX ? UINTPTR_MAX : static_cast<uintptr_t>(hi)};
+}
+bool meet(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// A stride in elements; larger ones than 2^40 are no tensor's.
+bool stride_ok(int64_t s) { return s >= 0 && s <= (static_cast<int64_t>(1) << 40); }
+
+// Output rows of `row` values must not share elements: each stride of more
+// than one entry is at least a row, and sorted strides nest.
+bool disjoint(int64_t row, int64_t na, int64_t sa, int64_t nb, int64_t sb, int64_t nc = 1,
+              int64_t sc = 0) {
+  int64_t n[3] = {na, nb, nc}, s[3] = {sa, sb, sc};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[j] < s[i]) {
+        const int64_t t = s[i], u = n[i];
+        s[i] = s[j], n[i] = n[j], s[j] = t, n[j] = u;
+      }
+  int64_t reach = row;
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (s[i] < reach) return false;
+    reach = (n[i] - 1) * s[i] + reach;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------------ rotary
+
+int bsa_rotary_freqs(int32_t pairs, double base, int32_t scaling, double factor,
+                     double trained_length, double fast_turns, double slow_turns, double* freqs,
+                     float* scale) {
+  if (pairs < 0 || pairs > 64 || (pairs > 0 && !freqs) || !scale) return BSA_ERR_INVALID;
+  if (!(base > 1.0) || !std::isfinite(base)) return BSA_ERR_INVALID;
+  if (scaling < BSA_ROPE_PLAIN || scaling > BSA_ROPE_BY_PARTS) return BSA_ERR_INVALID;
+  const bool by_parts = scaling == BSA_ROPE_YARN || scaling == BSA_ROPE_BY_PARTS;
+  if (scaling != BSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return BSA_ERR_INVALID;
+  if (by_parts && (!(trained_length >= 1.0) || !std::isfinite(trained_length) ||
+                   !(fast_turns > slow_turns) || !(slow_turns >= 0.0) ||
+                   !std::isfinite(fast_turns)))
+    return BSA_ERR_INVALID;
+  const double two_pi = 6.283185307179586476925286766559;
+  if (scaling == BSA_ROPE_NTK && pairs > 1)
+    base *= std::pow(factor, static_cast<double>(pairs) / (pairs - 1));
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -static_cast<double>(i) / pairs);
+    if (scaling == BSA_ROPE_LINEAR) f /= factor;
+    if (by_parts) {
+      // share of the pair's own frequency: 1 from fast_turns over the trained
+      // length on, 0 up to slow_turns
+      const double turns = trained_length * f / two_pi;
+      double keep = (turns - slow_turns) / (fast_turns - slow_turns);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    freqs[i] = f;
+  }
+  *scale = scaling == BSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return BSA_OK;
+}
+
+int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, const void* v,
+               const int32_t* positions, const double* freqs, const float* q_weight,
+               const float* k_weight, void* Q, void* K, void* V, void* stream) {
+  if (!params) return BSA_ERR_INVALID;
+  bsa_rotary_params own = *params;
+  bsa_rotary_params* p = &own;
+  if (p->D != 128 || p->B < 1 || p->H < 1 || p->N < 1 || p->N > kMaxN) return BSA_ERR_INVALID;
+  if (static_cast<int64_t>(p->B) * 3 > kMaxGrid || p->H > kMaxGrid) return BSA_ERR_INVALID;
+  if (p->rotary_dim < 0 || p->rotary_dim > 128 || p->rotary_dim % 2) return BSA_ERR_INVALID;
+  if (p->layout != BSA_ROPE_HALF && p->layout != BSA_ROPE_INTERLEAVED) return BSA_ERR_INVALID;
+  if (p->axes < 1 || p->axes > 4) return BSA_ERR_INVALID;
+  if (!float_type(p->in_dtype) || !float_type(p->out_dtype)) return BSA_ERR_INVALID;
+  if (!std::isfinite(p->scale) || !(p->eps >= 0.f) || !std::isfinite(p->eps))
+    return BSA_ERR_INVALID;
+  bsa::RotaryArgs a = {};
+  int pairs = 0;
+  for (int i = 0; i < p->axes; ++i) {
+    if (p->axis_pairs[i] < 0 || p->axis_pairs[i] > 64) return BSA_ERR_INVALID;
+    pairs += p->axis_pairs[i];
+    a.axis_end[i] = pairs;
+  }
+  if (2 * pairs != p->rotary_dim) return BSA_ERR_INVALID;
+  if (p->inverse && (q_weight || k_weight)) return BSA_ERR_INVALID;
+  // the stride of a single entry is never used
+  if (p->B == 1) p->in_b = p->out_b = p->pos_b = 0;
+  if (p->H == 1) p->in_h = p->out_h = 0;
+  if (p->N == 1) p->in_n = p->out_n = p->pos_n = 0;
+  for (int64_t s : {p->in_b, p->in_h, p->in_n, p->out_b, p->out_h, p->out_n, p->pos_b, p->pos_n})
+    if (!stride_ok(s)) return BSA_ERR_INVALID;
+  if (!disjoint(128, p->B, p->out_b, p->H, p->out_h, p->N, p->out_n)) return BSA_ERR_INVALID;
+  const void* in[3] = {q, k, v};
+  void* out[3] = {Q, K, V};
+  const float* weight[3] = {q_weight, k_weight, nullptr};
+  const int si = type_size(p->in_dtype), so = type_size(p->out_dtype);
+  const bool same = si == so && p->in_b == p->out_b && p->in_h == p->out_h && p->in_n == p->out_n;
+  for (int i = 0; i < 3; ++i) {
+    if ((in[i] == nullptr) != (out[i] == nullptr)) return BSA_ERR_INVALID;
+    if (!in[i]) {
+      if (weight[i]) return BSA_ERR_INVALID;
+      continue;
+    }
+    a.in[a.ntens] = in[i];
+    a.out[a.ntens] = out[i];
+    a.weight[a.ntens] = weight[i];
+    a.turn[a.ntens] = i < 2;
+    ++a.ntens;
+  }
+  if (a.ntens == 0) return BSA_ERR_INVALID;
+  if (p->rotary_dim > 0 && (q || k) && (!positions || !freqs)) return BSA_ERR_INVALID;
+  // Outputs: on their own input exactly, or apart from every input and output.
+  for (int i = 0; i < a.ntens; ++i) {
+    const bool in_place = a.out[i] == a.in[i] && same;
+    const Range ro = range_of(a.out[i], so, 128, p->B, p->out_b, p->H, p->out_h, p->N, p->out_n);
+    for (int j = 0; j < a.ntens; ++j) {
+      if (j != i && a.out[i] == a.out[j]) return BSA_ERR_INVALID;
+      if (in_place) continue;
+      const Range ri = range_of(a.in[j], si, 128, p->B, p->in_b, p->H, p->in_h, p->N, p->in_n);
+      if (meet(ro, ri)) return BSA_ERR_INVALID;
+    }
+  }
+  for (int i = 0; i < a.ntens; ++i)
+    if (!aligned(a.in[i], 16) || !aligned(a.out[i], 16) ||
+        (a.weight[i] && !aligned(a.weight[i], 16)))
+      return BSA_ERR_ALIGN;
+  for (int64_t s : {p->in_b, p->in_h, p->in_n})
+    if (s * si % 16) return BSA_ERR_ALIGN;
+  for (int64_t s : {p->out_b, p->out_h, p->out_n})
+    if (s * so % 16) return BSA_ERR_ALIGN;
+  if ((positions && !aligned(positions, 4)) || (freqs && !aligned(freqs, 8))) return BSA_ERR_ALIGN;
+  int rc = check_device();
+  if (rc) return rc;
+  a.B = p->B, a.H = p->H, a.N = p->N, a.r = p->rotary_dim;
+  a.interleaved = p->layout == BSA_ROPE_INTERLEAVED;
+  a.scale = p->scale;
+  a.sin_scale = p->inverse ? -p->scale : p->scale;
+  a.eps = p->eps;
+  a.in_b = p->in_b, a.in_h = p->in_h, a.in_n = p->in_n;
+  a.out_b = p->out_b, a.out_h = p->out_h, a.out_n = p->out_n;
+  a.pos_b = p->pos_b, a.pos_n = p->pos_n;
+  a.positions = positions;
+  a.freqs = freqs;
+  return cuda_status(bsa::launch_rotary(a, p->in_dtype == BSA_DTYPE_FP32,
+                                        p->out_dtype == BSA_DTYPE_FP32,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ gate norm
+
+int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,
+                  float* z_scale, void* stream) {
+  if (!params || !in) return BSA_ERR_INVALID;
+  bsa_gate_norm_params own = *params;
+  bsa_gate_norm_params* p = &own;
+  if (p->B < 1 || p->N < 1 || p->C < 1 || p->C > kMaxRow) return BSA_ERR_INVALID;
+  for (int kind : {p->pre, p->post})
+    if (kind < BSA_NORM_NONE || kind > BSA_NORM_LAYER) return BSA_ERR_INVALID;
+  if (!float_type(p->x_dtype) || !float_type(p->y_dtype) || !float_type(p->mod_dtype))
+    return BSA_ERR_INVALID;
+  if (!float_type(p->z_dtype) && p->z_dtype != BSA_DTYPE_INT8) return BSA_ERR_INVALID;
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps) || !std::isfinite(p->residual_scale) ||
+      !std::isfinite(p->branch_scale))
+    return BSA_ERR_INVALID;
+  if (!in->x || (!h && !z)) return BSA_ERR_INVALID;
+  if (!in->y && (h || in->gate || in->post_weight || in->post_bias)) return BSA_ERR_INVALID;
+  if (!z && (in->scale || in->shift || in->pre_weight || in->pre_bias)) return BSA_ERR_INVALID;
+  if ((z && p->z_dtype == BSA_DTYPE_INT8) != (z_scale != nullptr)) return BSA_ERR_INVALID;
+  // the stride of a single entry is never used
+  if (p->B == 1)
+    p->x_b = p->y_b = p->h_b = p->z_b = p->gate_b = p->scale_b = p->shift_b = 0;
+  if (p->N == 1)
+    p->x_n = p->y_n = p->h_n = p->z_n = p->gate_n = p->scale_n = p->shift_n = 0;
+  for (int64_t s : {p->x_b, p->x_n, p->y_b, p->y_n, p->h_b, p->h_n, p->z_b, p->z_n, p->gate_b,
+                    p->gate_n, p->scale_b, p->scale_n, p->shift_b, p->shift_n})
+    if (!stride_ok(s)) return BSA_ERR_INVALID;
+  const int sx = type_size(p->x_dtype), sy = type_size(p->y_dtype), sm = type_size(p->mod_dtype),
+            sz = type_size(p->z_dtype);
+  if (h && !disjoint(p->C, p->B, p->h_b, p->N, p->h_n)) return BSA_ERR_INVALID;
+  if (z && !disjoint(p->C, p->B, p->z_b, p->N, p->z_n)) return BSA_ERR_INVALID;
+  // h may be x itself (the residual updated in place); any other overlap of an
+  // output is refused.
+  const Range rx = range_of(in->x, sx, p->C, p->B, p->x_b, p->N, p->x_n);
+  const Range ry = in->y ? range_of(in->y, sy, p->C, p->B, p->y_b, p->N, p->y_n) : Range{0, 0};
+  const Range rh = h ? range_of(h, sx, p->C, p->B, p->h_b, p->N, p->h_n) : Range{0, 0};
+  const Range rz = z ? range_of(z, sz, p->C, p->B, p->z_b, p->N, p->z_n) : Range{0, 0};
+  const bool in_place = h == in->x && p->h_b == p->x_b && p->h_n == p->x_n;
+  if (h && ((!in_place && meet(rh, rx)) || meet(rh, ry) || meet(rh, rz))) return BSA_ERR_INVALID;
+  if (z && (meet(rz, rx) || meet(rz, ry))) return BSA_ERR_INVALID;
+  if (!aligned(in->x, sx) || (in->y && !aligned(in->y, sy)) || (h && !aligned(h, sx)) ||
+      (z && !aligned(z, sz)) || (z_scale && !aligned(z_scale, 4)))
+    return BSA_ERR_ALIGN;
+  for (const void* m : {in->gate, in->scale, in->shift})
+    if (m && !aligned(m, sm)) return BSA_ERR_ALIGN;
+  for (const float* w : {in->post_weight, in->post_bias, in->pre_weight, in->pre_bias})
+    if (w && !aligned(w, 4)) return BSA_ERR_ALIGN;
+  int rc = check_device();
+  if (rc) return rc;
+  bsa::GateNormArgs a = {};
+  a.x = in->x, a.y = in->y, a.gate = in->gate, a.mscale = in->scale, a.shift = in->shift;
+  a.post_weight = in->post_weight, a.post_bias = in->post_bias;
+  a.pre_weight = in->pre_weight, a.pre_bias = in->pre_bias;
+  a.h = h, a.z = z, a.z_scale = z_scale;
+  a.B = p->B, a.N = p->N, a.C = p->C, a.pre = p->pre, a.post = p->post;
+  a.y_fp32 = p->y_dtype == BSA_DTYPE_FP32, a.mod_fp32 = p->mod_dtype == BSA_DTYPE_FP32;
+  a.z_type = p->z_dtype;
+  a.eps = p->eps, a.residual_scale = p->residual_scale, a.branch_scale = p->branch_scale;
+  a.x_b = p->x_b, a.x_n = p->x_n, a.y_b = p->y_b, a.y_n = p->y_n, a.h_b = p->h_b, a.h_n = p->h_n;
+  a.z_b = p->z_b, a.z_n = p->z_n, a.gate_b = p->gate_b, a.gate_n = p->gate_n;
+  a.scale_b = p->scale_b, a.scale_n = p->scale_n, a.shift_b = p->shift_b, a.shift_n = p->shift_n;
+  // 16-byte words where every row of every operand starts on one (8 codes make 8 bytes)
+  bool vec = p->C % 8 == 0;
+  auto rows16 = [&](const void* base, int size, int64_t sb, int64_t sn) {
+    if (base) vec = vec && aligned(base, 8 * size < 16 ? 8 * size : 16) && sb % 8 == 0 && sn % 8 == 0;
+  };
+  rows16(in->x, sx, p->x_b, p->x_n);
+  rows16(in->y, sy, p->y_b, p->y_n);
+  rows16(h, sx, p->h_b, p->h_n);
+  rows16(z, sz, p->z_b, p->z_n);
+  rows16(in->gate, sm, p->gate_b, p->gate_n);
+  rows16(in->scale, sm, p->scale_b, p->scale_n);
+  rows16(in->shift, sm, p->shift_b, p->shift_n);
+  for (const float* w : {in->post_weight, in->post_bias, in->pre_weight, in->pre_bias})
+    rows16(w, 4, 0, 0);
+  return cuda_status(bsa::launch_gate_norm(a, p->x_dtype == BSA_DTYPE_FP32, vec,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ int8
+
+int bsa_quantize_int8(const bsa_quantize_int8_params* params, const void* x, int8_t* codes, float* scale,
+                      void* stream) {
+  if (!params) return BSA_ERR_INVALID;
+  bsa_quantize_int8_params own = *params;
+  bsa_quantize_int8_params* p = &own;
+  if (p->B < 1 || p->N < 1 || p->S < 1 || p->L < 1) return BSA_ERR_INVALID;
+  if (static_cast<int64_t>(p->S) * p->L > kMaxRow) return BSA_ERR_INVALID;
+  if (static_cast<int64_t>(p->B) * p->N > INT32_MAX) return BSA_ERR_INVALID;
+  if (!float_type(p->x_dtype)) return BSA_ERR_INVALID;
+  if (!x || !codes || !scale) return BSA_ERR_INVALID;
+  // the stride of a single entry is never used
+  if (p->B == 1) p->x_b = 0;
+  if (p->N == 1) p->x_n = 0;
+  if (p->S == 1) p->x_s = 0;
+  if (p->B == 1 && p->N == 1) p->ld = static_cast<int64_t>(p->S) * p->L;
+  for (int64_t s : {p->x_b, p->x_n, p->x_s, p->ld})
+    if (!stride_ok(s)) return BSA_ERR_INVALID;
+  const int64_t K = static_cast<int64_t>(p->S) * p->L;
+  const int64_t rows = static_cast<int64_t>(p->B) * p->N;
+  if (p->ld < K) return BSA_ERR_INVALID;
+  const int sx = type_size(p->x_dtype);
+  if (meet(range_of(x, sx, p->L, p->B, p->x_b, p->N, p->x_n, p->S, p->x_s),
+           range_of(codes, 1, K, rows, p->ld)))
+    return BSA_ERR_INVALID;
+  if (!aligned(x, sx) || !aligned(scale, 4)) return BSA_ERR_ALIGN;
+  int rc = check_device();
+  if (rc) return rc;
+  bsa::QuantInt8Args a = {};
+  a.x = x, a.q = codes, a.scale = scale;
+  a.B = p->B, a.N = p->N, a.S = p->S, a.L = p->L;
+  a.x_b = p->x_b, a.x_n = p->x_n, a.x_s = p->x_s, a.q_ld = p->ld;
+  const bool vec = p->L % 8 == 0 && aligned(x, 16) && aligned(codes, 8) &&
+                   p->x_b % 8 == 0 && p->x_n % 8 == 0 && p->x_s % 8 == 0 &&
+                   (rows == 1 || p->ld % 8 == 0);
+  return cuda_status(bsa::launch_quant_int8(a, p->x_dtype == BSA_DTYPE_FP32, vec,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const float* a_scale,
+                    const int8_t* w, const float* w_scale, const float* bias, void* out,
+                    void* stream) {
+  if (!params) return BSA_ERR_INVALID;
+  bsa_linear_int8_params own = *params;
+  bsa_linear_int8_params* p = &own;
+  if (p->M < 1 || p->N < 1 || p->K < 1 || p->K > kMaxRow) return BSA_ERR_INVALID;
+  if (!float_type(p->out_dtype)) return BSA_ERR_INVALID;
+  if (!a || !a_scale || !w || !w_scale || !out) return BSA_ERR_INVALID;
+  // the stride of a single row is never used
+  if (p->M == 1) p->lda = (p->K + 15) / 16 * 16, p->ldo = p->N;
+  if (p->N == 1) p->ldw = (p->K + 15) / 16 * 16;
+  for (int64_t s : {p->lda, p->ldw, p->ldo})
+    if (!stride_ok(s)) return BSA_ERR_INVALID;
+  if (p->lda < p->K || p->ldw < p->K || p->ldo < p->N) return BSA_ERR_INVALID;
+  const int so = type_size(p->out_dtype);
+  const Range ro = range_of(out, so, p->N, p->M, p->ldo);
+  if (meet(ro, range_of(a, 1, p->K, p->M, p->lda)) || meet(ro, range_of(w, 1, p->K, p->N, p->ldw)))
+    return BSA_ERR_INVALID;
+  if (!aligned(a, 16) || !aligned(w, 16) || p->lda % 16 || p->ldw % 16 || !aligned(out, so) ||
+      !aligned(a_scale, 4) || !aligned(w_scale, 4) || (bias && !aligned(bias, 4)))
+    return BSA_ERR_ALIGN;
+  int rc = check_device();
+  if (rc) return rc;
+  bsa::EncodeTiledFn enc = bsa::encode_fn();
+  if (!enc) return BSA_ERR_UNSUPPORTED;
+  // rows of K bytes, `box` of them 128 bytes wide; what lies past K or the
+  // last row reads as zero
+  auto map = [&](CUtensorMap* m, const int8_t* base, int rows, int64_t ld, int box) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p->K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+    const cuuint32_t b[2] = {128, static_cast<cuuint32_t>(box)}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims, strides, b,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  int box_a, box_w;
+  bsa::linear_int8_boxes(p->M, &box_a, &box_w);
+  CUtensorMap ma, mw;
+  if (!map(&ma, a, p->M, p->lda, box_a) || !map(&mw, w, p->N, p->ldw, box_w))
+    return BSA_ERR_UNSUPPORTED;
+  bsa::LinearInt8Args l = {};
+  l.M = p->M, l.N = p->N, l.K = p->K;
+  l.a_scale = a_scale, l.w_scale = w_scale, l.bias = bias;
+  l.out = out, l.ldo = p->ldo, l.out_fp32 = p->out_dtype == BSA_DTYPE_FP32;
+  l.dev_status = p->dev_status;
+  return cuda_status(bsa::launch_linear_int8(l, ma, mw, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -171,6 +171,69 @@ cudaError_t launch_extra_summaries(const Shape& s, int n_extra, const void* K, c
                                    float* side_bias, int32_t* side_blk, int32_t* side_cnt,
                                    cudaStream_t st);
 
+// ---- the operators around the attention --------------------------------
+
+enum { kTypeBf16 = 0, kTypeFp32 = 1, kTypeInt8 = 2 };   // == bsa_dtype
+enum { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };   // == bsa_norm
+
+// Rotary positions (rotary.cu).  ntens tensors of B x H x N rows of 128; `turn`
+// 0 copies the row (v).  Strides in elements; tt and hchunk are set by the
+// launcher.
+struct RotaryArgs {
+  const void* in[3];
+  void* out[3];
+  const float* weight[3];
+  int turn[3];
+  int ntens;
+  int B, H, N, r, interleaved;
+  int axis_end[4];               // pairs before the end of each axis
+  float scale, sin_scale, eps;
+  int64_t in_b, in_h, in_n, out_b, out_h, out_n, pos_b, pos_n;
+  const int32_t* positions;
+  const double* freqs;
+  int tt, hchunk;
+};
+cudaError_t launch_rotary(RotaryArgs a, int in_fp32, int out_fp32, cudaStream_t st);
+
+// Gated and modulated norms (gate_norm.cu); pointers that are NULL are left out.
+struct GateNormArgs {
+  const void *x, *y, *gate, *mscale, *shift;
+  const float *post_weight, *post_bias, *pre_weight, *pre_bias;
+  void *h, *z;
+  float* z_scale;
+  int B, N, C, pre, post, y_fp32, mod_fp32, z_type;
+  float eps, residual_scale, branch_scale;
+  int64_t x_b, x_n, y_b, y_n, h_b, h_n, z_b, z_n;
+  int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;
+};
+cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, bool vec, cudaStream_t st);
+
+// Row quantisation (quant_int8.cu): B x N rows of S segments of L values.
+struct QuantInt8Args {
+  const void* x;
+  int8_t* q;
+  float* scale;
+  int B, N, S, L;
+  int64_t x_b, x_n, x_s, q_ld;
+};
+cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cudaStream_t st);
+// Threads and 8-value chunks a thread of a row of n values (gate_norm.cu).
+void row_shape(int n, int64_t rows, int* ch, int* threads);
+
+// int8 product (linear_int8.cu): out[m, n] = a_scale[m] w_scale[n] sum_k a[m, k] w[n, k] + bias[n].
+struct LinearInt8Args {
+  int M, N, K;
+  const float *a_scale, *w_scale, *bias;
+  void* out;
+  int64_t ldo;
+  int out_fp32;
+  int* dev_status;
+};
+// Rows of the tensor maps' boxes (128 bytes wide) of the tokens and the weights.
+void linear_int8_boxes(int M, int* box_a, int* box_w);
+cudaError_t launch_linear_int8(const LinearInt8Args& a, const CUtensorMap& ma,
+                               const CUtensorMap& mw, cudaStream_t st);
+
 cudaError_t launch_expired_wait(int32_t* dev_status, uint64_t timeout_ns, cudaStream_t st);
 
 }  // namespace bsa

@@ -497,6 +497,156 @@ int bsa_forward_extra(const bsa_params* p, int32_t n_extra, const void* Q, const
                       const void* V, void* O, float* lse, void* workspace, size_t workspace_bytes,
                       void* stream);
 
+/* ---- the operators around the attention --------------------------------
+ *
+ * A block's hidden states are token rows [B, N, C]; the attention takes
+ * [B, H, N, 128].  These entry points are what lies between: the modulated
+ * norm before the projection, the projections on int8 operands, the rotary
+ * positions with the head-major layout, and the gated residual after.  The
+ * pages name no numerics for them (they patch an existing model); the formulas
+ * are this library's, stated at each.
+ *
+ * Conventions beside the general ones: strides are in elements, non-negative,
+ * and that of a dimension of one entry is ignored; the fastest dimension is
+ * contiguous.  Sums, norms and angles are fp32 or wider, and every output is
+ * rounded once, to nearest even.  Outputs do not overlap inputs or each other
+ * except where an entry says that it works in place (an overlap of the large
+ * operands is BSA_ERR_INVALID).  Calls are deterministic, keep no state and
+ * can be captured into CUDA graphs. */
+
+typedef enum {
+  BSA_DTYPE_BF16 = 0,
+  BSA_DTYPE_FP32 = 1,
+  BSA_DTYPE_INT8 = 2
+} bsa_dtype;
+
+typedef enum {
+  BSA_ROPE_HALF = 0,        /* pair i is dimensions i and i + rotary_dim / 2  */
+  BSA_ROPE_INTERLEAVED = 1  /* pair i is dimensions 2 i and 2 i + 1           */
+} bsa_rope_layout;
+
+typedef enum {
+  BSA_ROPE_PLAIN = 0,
+  BSA_ROPE_LINEAR = 1,   /* f / factor                                       */
+  BSA_ROPE_NTK = 2,      /* base * factor^(pairs / (pairs - 1))              */
+  BSA_ROPE_YARN = 3,     /* by parts, and scale = 0.1 ln factor + 1          */
+  BSA_ROPE_BY_PARTS = 4  /* f from fast_turns over the trained length on,
+                            f / factor up to slow_turns, linear between      */
+} bsa_rope_scaling;
+
+/* Frequencies of one axis, on the HOST: freqs[i] = base^(-i / pairs) radians a
+ * position for i < pairs (0 <= pairs <= 64), changed for long contexts by
+ * `scaling` with factor >= 1 (1 for PLAIN is not looked at).  YARN and
+ * BY_PARTS mix each pair by the turns it makes over trained_length positions,
+ * fast_turns > slow_turns >= 0; the others ignore those three.  *scale is the
+ * factor on cos and sin that goes with it.  The caller copies freqs to the
+ * device once. */
+int bsa_rotary_freqs(int32_t pairs, double base, int32_t scaling, double factor,
+                     double trained_length, double fast_turns, double slow_turns, double* freqs,
+                     float* scale);
+
+typedef struct {
+  int32_t B, H, N, D;      /* D must be 128; B, H, N as bsa_params, B <= 21845 */
+  int32_t rotary_dim;      /* even, 0..128: dimensions past it pass unchanged */
+  int32_t layout;          /* bsa_rope_layout                                 */
+  int32_t axes;            /* 1..4 position axes (t, h, w, ..)                */
+  int32_t axis_pairs[4];   /* pairs of each axis in turn, rotary_dim / 2 in all */
+  int32_t inverse;         /* non-zero: turn by -theta (the transposed map)   */
+  int32_t in_dtype, out_dtype;   /* bsa_dtype: bf16 or fp32                   */
+  float scale;             /* m, on cos and sin                               */
+  float eps;               /* of the RMS norm                                 */
+  int64_t in_b, in_h, in_n;      /* strides of q, k and v                     */
+  int64_t out_b, out_h, out_n;   /* strides of Q, K and V                     */
+  int64_t pos_b, pos_n;          /* strides of positions, axes contiguous     */
+} bsa_rotary_params;
+
+/* Rotary positions.  For every row x (128 dimensions of head h, token n) of q
+ * and k: with a weight, x <- x rsqrt(mean(x^2) + eps) weight first (fp32
+ * [128], one for q and one for k); then pair i of axis a turns by theta =
+ * positions[b, n, a] * freqs[i], (x0, x1) -> m (x0 cos theta - x1 sin theta,
+ * x1 cos theta + x0 sin theta).  v is copied.  Any of q, k, v may be NULL with
+ * its output.  positions int32 (negative ones too), freqs fp64 [rotary_dim /
+ * 2] in radians; angles are kept as fixed-point turns, so far positions lose
+ * nothing.  inverse takes no weights.
+ * Q may be q itself with the same strides and type (in place), K and V
+ * likewise.  Bases and strides are multiples of 16 bytes.
+ * Token-major projections [B, N, 3, H, 128] to head-major [B, H, N, 128] are
+ * one call: one read and one write of every row. */
+int bsa_rotary(const bsa_rotary_params* p, const void* q, const void* k, const void* v,
+               const int32_t* positions, const double* freqs, const float* q_weight,
+               const float* k_weight, void* Q, void* K, void* V, void* stream);
+
+typedef enum { BSA_NORM_NONE = 0, BSA_NORM_RMS = 1, BSA_NORM_LAYER = 2 } bsa_norm;
+
+typedef struct {
+  int32_t B, N, C;               /* rows B x N of C values, C <= 32768        */
+  int32_t pre, post;             /* bsa_norm                                  */
+  int32_t x_dtype;               /* of x and h: bf16 or fp32                  */
+  int32_t y_dtype;               /* bf16 or fp32                              */
+  int32_t mod_dtype;             /* of gate, scale and shift: bf16 or fp32    */
+  int32_t z_dtype;               /* bf16, fp32 or int8                        */
+  float eps, residual_scale, branch_scale;
+  int64_t x_b, x_n, y_b, y_n, h_b, h_n, z_b, z_n;
+  int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;  /* 0: shared   */
+} bsa_gate_norm_params;
+
+typedef struct {
+  const void* x;             /* residual stream                               */
+  const void* y;             /* the block's output, or NULL                   */
+  const void* gate;          /* on y, or NULL (1)                             */
+  const void* scale;         /* modulation of z, or NULL (0)                  */
+  const void* shift;         /* or NULL (0)                                   */
+  const float* post_weight;  /* fp32 [C], each may be NULL                    */
+  const float* post_bias;
+  const float* pre_weight;
+  const float* pre_bias;
+} bsa_gate_norm_inputs;
+
+/* Norms before and after a block with its gate and residual, in one pass:
+ *   h = residual_scale x + branch_scale gate post(y)      (h = x without y)
+ *   z = pre(h) (1 + scale) + shift
+ * post and pre: nothing, v rsqrt(mean(v^2) + eps), or (v - mean(v))
+ * rsqrt(mean((v - mean(v))^2) + eps), then weight and bias where given.  z is
+ * formed from h before its rounding.  h is written when non-NULL (it needs y),
+ * z when non-NULL.  z_dtype int8: codes and z_scale [B N] as
+ * bsa_quantize_int8 makes them; z_scale is NULL otherwise.  h may be x with
+ * the same strides (in place). */
+int bsa_gate_norm(const bsa_gate_norm_params* p, const bsa_gate_norm_inputs* in, void* h, void* z,
+                  float* z_scale, void* stream);
+
+typedef struct {
+  int32_t B, N, S, L;        /* rows B x N of S segments of L values, S L <= 32768 */
+  int32_t x_dtype;           /* bf16 or fp32                                  */
+  int64_t x_b, x_n, x_s;     /* strides of entry, row and segment             */
+  int64_t ld;                /* stride of the code rows, >= S L               */
+} bsa_quantize_int8_params;
+
+/* int8 codes of rows, one scale a row: amax = max(max |x|, 2^-100),
+ * scale = fp32(amax / 127), code = round-to-even(fp32(x * fp32(127 / amax))).
+ * A row with a NaN or an infinity gets scale NaN and codes 0.  codes [B N, ld]
+ * (bytes past S L of a row are left as they are), scale fp32 [B N].  With S =
+ * H, L = 128 and the strides of [B, H, N, 128] the attention's output becomes
+ * token rows of H 128 values.  Weights [N, K]: B = 1, S = 1, L = K. */
+int bsa_quantize_int8(const bsa_quantize_int8_params* p, const void* x, int8_t* codes, float* scale,
+                      void* stream);
+
+typedef struct {
+  int32_t M, N, K;           /* tokens, output channels, input channels <= 32768 */
+  int32_t out_dtype;         /* bf16 or fp32                                  */
+  int64_t lda, ldw;          /* bytes from row to row, multiples of 16, >= K  */
+  int64_t ldo;               /* elements from row to row of out, >= N         */
+  int32_t* dev_status;       /* as bsa_params                                 */
+} bsa_linear_int8_params;
+
+/* out[m, n] = a_scale[m] w_scale[n] sum_k a[m, k] w[n, k] + bias[n] (bias fp32
+ * [N] or NULL).  The sum is exact (int32 in tcgen05's kind::i8); scales, bias
+ * and one rounding follow in fp32, so the result does not depend on how the
+ * product is split.  a and w start on 16 bytes; bytes between K and the row
+ * stride are not read into the sum. */
+int bsa_linear_int8(const bsa_linear_int8_params* p, const int8_t* a, const float* a_scale,
+                    const int8_t* w, const float* w_scale, const float* bias, void* out,
+                    void* stream);
+
 /* Human-readable name of a bsa_status value (static string). */
 const char* bsa_status_string(int status);
 

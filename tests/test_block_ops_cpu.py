@@ -1,0 +1,252 @@
+"""The operators around the attention without a GPU: the oracle against independent forms, the host-side
+frequency helper, and the refusals that come before any launch."""
+
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_video_bsa_b200 import bsa
+from oracle import bsa_oracle_block as orb
+
+
+# ------------------------------------------------------------------ oracle pins
+
+def test_turns_reduce_far_positions_exactly():
+    # sin(p) of whole radians far out, against known identities: angle addition with exact small parts
+    f = np.array([1.0, 0.5, 1e-4])
+    for p in (0, 1, 7, 10 ** 6, 2 ** 31 - 1, -(2 ** 31)):
+        t = orb.turns(np.array([[p, p, p]]), f)
+        assert (t >= 0).all() and (t < 2 * math.pi + 1e-12).all()
+        for i in range(3):
+            # Python's own argument reduction of the exact product is right to the product's rounding
+            assert abs(math.remainder(t[0, i] - p * f[i], 2 * math.pi)) <= abs(p * f[i]) * 2.0 ** -52 + 1e-15
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("r", [2, 10, 96, 128])
+def test_rotary_oracle_is_complex_multiplication(layout, r):
+    g = np.random.default_rng(0)
+    x = g.standard_normal((2, 5, 128))
+    pos = g.integers(-50, 50, (5, 1))
+    f, _ = orb.rotary_freqs(r // 2)
+    y = orb.rotary(x, pos, f, layout, [r // 2])
+    a = x[..., :r].reshape(2, 5, 2, r // 2).swapaxes(-1, -2) if layout == "half" else x[..., :r].reshape(2, 5, r // 2, 2)
+    z = (a[..., 0] + 1j * a[..., 1]) * np.exp(1j * pos * f)
+    b = y[..., :r].reshape(2, 5, 2, r // 2).swapaxes(-1, -2) if layout == "half" else y[..., :r].reshape(2, 5, r // 2, 2)
+    assert np.abs(b[..., 0] - z.real).max() < 1e-12 and np.abs(b[..., 1] - z.imag).max() < 1e-12
+    assert (y[..., r:] == x[..., r:]).all()
+    back = orb.rotary(y, pos, f, layout, [r // 2], inverse=True)
+    assert np.abs(back - x).max() < 1e-12
+
+
+def test_rotary_oracle_depends_on_position_differences_only():
+    g = np.random.default_rng(1)
+    q, k = g.standard_normal((1, 1, 128)), g.standard_normal((1, 1, 128))
+    f, _ = orb.rotary_freqs(64)
+    dot = lambda p, s: float((orb.rotary(q, np.array([[p]]), f, "half", [64]) * orb.rotary(k, np.array([[s]]), f, "half", [64])).sum())  # noqa: E731
+    assert abs(dot(10, 3) - dot(1_000_010, 1_000_003)) < 1e-9
+
+
+@pytest.mark.parametrize("post", ["none", "rms", "layer"])
+@pytest.mark.parametrize("pre", ["none", "rms", "layer"])
+def test_gate_norm_oracle_against_torch(pre, post):
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    x, y, gate, scale, shift = r(3, 40), r(3, 40), r(40), r(40), r(40)
+    w, b, w2, b2 = r(40), r(40), r(40), r(40)
+
+    def norm(v, kind, w, b):
+        if kind == "layer":
+            return torch.nn.functional.layer_norm(v, (40,), w, b, 1e-6)
+        v = torch.nn.functional.rms_norm(v, (40,), None, 1e-6) if kind == "rms" else v
+        return v * w + b
+    h = 0.5 * x + 2.0 * gate * norm(y, post, w, b)
+    z = norm(h, pre, w2, b2) * (1 + scale) + shift
+    n = lambda t: t.numpy()  # noqa: E731
+    h2, z2 = orb.gate_norm(n(x), n(y), n(gate), n(scale), n(shift), pre, n(w2), n(b2), post, n(w), n(b), 1e-6, 0.5, 2.0)
+    assert np.abs(h2 - n(h)).max() < 1e-12 and np.abs(z2 - n(z)).max() < 1e-11
+
+
+def test_int8_rows_of_the_oracle():
+    g = np.random.default_rng(2)
+    x = torch.from_numpy(g.standard_normal((6, 33)).astype(np.float32)).bfloat16().float().numpy()
+    x[1] = 0.0
+    x[2, 5] = np.inf
+    x[3, 0] = np.nan
+    x[4] *= 1e-38
+    codes, scales = orb.quantize_int8(x)
+    assert np.abs(codes).max() == 127
+    for m in (0, 5):
+        assert np.abs(codes[m] * scales[m].astype(np.float64) - x[m]).max() <= 0.5 * scales[m] * (1 + 2.0 ** -20)
+        assert np.abs(codes[m]).max() == 127
+    for m in (1, 4):      # below the floor: zero within the floor's step
+        assert scales[m] == np.float32(orb.INT8_FLOOR / 127) and not codes[m].any()
+    for m in (2, 3):
+        assert np.isnan(scales[m]) and not codes[m].any()
+
+
+def test_linear_oracle_sums_are_whole():
+    a = np.full((2, 32768), -127, np.int8)
+    w = np.full((3, 32768), 127, np.int8)
+    out = orb.linear_int8(a, np.ones(2, np.float32), w, np.ones(3, np.float32))
+    assert (out == -127 * 127 * 32768).all() and 127 * 127 * 32768 < 2 ** 31
+
+
+# ------------------------------------------------------------------ frequencies (host)
+
+@pytest.mark.parametrize("scaling,factor", [("plain", 1.0), ("linear", 4.0), ("ntk", 8.0), ("yarn", 8.0), ("by_parts", 2.0)])
+@pytest.mark.parametrize("pairs", [1, 2, 21, 64])
+def test_frequencies_match_the_oracle(scaling, factor, pairs):
+    f, m = bsa.rotary_freqs(pairs, 10000.0, scaling, factor, 4096, device="cpu")
+    g, n = orb.rotary_freqs(pairs, 10000.0, scaling, factor, 4096.0)
+    assert f.dtype == torch.float64 and np.abs(f.numpy() / g - 1).max() < 1e-13
+    assert abs(m - n) <= n * 2.0 ** -24
+
+
+def test_frequencies_of_several_axes_and_ends():
+    f, _ = bsa.rotary_freqs([22, 21, 21], device="cpu")
+    assert f.shape == (64,) and f[0] == f[22] == f[43] == 1.0
+    f, m = bsa.rotary_freqs(64, 10000.0, "by_parts", 8.0, 4096, device="cpu")
+    p, _ = bsa.rotary_freqs(64, device="cpu")
+    assert f[0] == p[0] and m == 1.0                           # many turns: kept
+    assert abs(f[63] * 8 / p[63] - 1) < 1e-14                  # under one turn: divided
+    assert (f <= p).all() and (f >= p / 8).all()
+
+
+@pytest.mark.parametrize("kw", [dict(pairs=65), dict(pairs=-1), dict(base=1.0), dict(base=float("nan")),
+                                dict(scaling="linear", factor=0.5), dict(scaling="ntk", factor=float("inf")),
+                                dict(scaling="yarn", factor=2.0, trained_length=0),
+                                dict(scaling="yarn", factor=2.0, trained_length=4096, fast_turns=1.0, slow_turns=1.0),
+                                dict(scaling="by_parts", factor=2.0, trained_length=4096, slow_turns=-1.0)])
+def test_frequency_refusals(kw):
+    with pytest.raises(bsa.BsaError) as e:
+        bsa.rotary_freqs(**dict(dict(pairs=64, device="cpu"), **kw))
+    assert e.value.status == bsa.BSA_ERR_INVALID
+
+
+# ------------------------------------------------------------------ refusals before any launch
+
+A = 1 << 30       # pretend addresses: never dereferenced, every call below is refused
+BIG = 1 << 28
+
+
+def _rot(ptrs=None, **kw):
+    p = dict(B=1, H=4, N=100, D=128, rotary_dim=128, layout=0, axes=1, inverse=0, in_dtype=0, out_dtype=0,
+             scale=1.0, eps=1e-6, in_b=100 * 512, in_h=128, in_n=512, out_b=100 * 512, out_h=100 * 128, out_n=128,
+             pos_b=0, pos_n=1)
+    pairs = kw.pop("axis_pairs", (64,))
+    p.update(kw)
+    s = bsa.bsa_rotary_params(**p)
+    s.axis_pairs = (ctypes.c_int32 * 4)(*pairs)
+    a = dict(q=A, k=A + BIG, v=A + 2 * BIG, pos=A, freqs=A, qw=None, kw=None, Q=A + 3 * BIG, K=A + 4 * BIG, V=A + 5 * BIG)
+    a.update(ptrs or {})
+    return bsa.lib().bsa_rotary(ctypes.byref(s), *[a[n] for n in ("q", "k", "v", "pos", "freqs", "qw", "kw", "Q", "K", "V")], None)
+
+
+@pytest.mark.parametrize("kw", [dict(D=64), dict(B=0), dict(H=0), dict(N=0), dict(N=(1 << 21) + 1), dict(B=21846),
+                                dict(rotary_dim=130, axis_pairs=(65,)), dict(rotary_dim=3), dict(rotary_dim=-2), dict(layout=2),
+                                dict(axes=0), dict(axes=5), dict(axis_pairs=(63,)), dict(axes=2, axis_pairs=(65, -1)),
+                                dict(in_dtype=2), dict(out_dtype=3), dict(scale=float("nan")), dict(eps=-1.0), dict(eps=float("inf")),
+                                dict(in_n=-512), dict(out_n=64), dict(out_h=0), dict(pos_n=-1), dict(in_b=1 << 50)])
+def test_rotary_invalid_parameters(kw):
+    if "in_b" in kw:
+        kw = dict(kw, B=2)
+    assert _rot(**kw) == bsa.BSA_ERR_INVALID
+
+
+def test_rotary_pointers():
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    assert bsa.lib().bsa_rotary(None, *[None] * 10, None) == inv
+    assert _rot(dict(Q=None)) == inv and _rot(dict(q=None)) == inv
+    assert _rot(dict(q=None, k=None, v=None, Q=None, K=None, V=None)) == inv
+    assert _rot(dict(pos=None)) == inv and _rot(dict(freqs=None)) == inv
+    assert _rot(dict(qw=A), inverse=1) == inv
+    assert _rot(dict(q=None, Q=None, qw=A)) == inv                   # a weight without its rows
+    assert _rot(dict(Q=A)) == inv                                    # on its input, other strides
+    assert _rot(dict(Q=A + 1024)) == inv and _rot(dict(Q=A + BIG)) == inv     # into q, into k
+    assert _rot(dict(K=A + 3 * BIG)) == inv                          # two outputs in one place
+    assert _rot(dict(q=A + 8)) == al and _rot(dict(V=A + 5 * BIG + 4)) == al
+    assert _rot(dict(qw=A + 4)) == al and _rot(dict(freqs=A + 4)) == al and _rot(dict(pos=A + 2)) == al
+    assert _rot(in_n=513) == al and _rot(out_n=132, out_h=100 * 132) == al
+
+
+def _gn(inp=None, h=A + 2 * BIG, z=A + 3 * BIG, zs=None, **kw):
+    p = dict(B=2, N=10, C=256, pre=1, post=1, x_dtype=0, y_dtype=0, mod_dtype=1, z_dtype=0, eps=1e-6, residual_scale=1.0,
+             branch_scale=1.0)
+    for n in "xyhz":
+        p[n + "_b"], p[n + "_n"] = 2560, 256
+    for n in ("gate", "scale", "shift"):
+        p[n + "_b"], p[n + "_n"] = 256, 0
+    p.update(kw)
+    i = dict(x=A, y=A + BIG, gate=A, scale=A, shift=A)
+    i.update(inp or {})
+    return bsa.lib().bsa_gate_norm(ctypes.byref(bsa.bsa_gate_norm_params(**p)), ctypes.byref(bsa.bsa_gate_norm_inputs(**i)), h, z, zs, None)
+
+
+@pytest.mark.parametrize("kw", [dict(B=0), dict(N=0), dict(C=0), dict(C=32769), dict(pre=3), dict(post=-1), dict(x_dtype=2),
+                                dict(y_dtype=2), dict(mod_dtype=2), dict(z_dtype=3), dict(eps=-1e-6), dict(eps=float("nan")),
+                                dict(residual_scale=float("inf")), dict(branch_scale=float("nan")), dict(x_n=-1),
+                                dict(h_n=255), dict(z_b=0)])
+def test_gate_norm_invalid_parameters(kw):
+    assert _gn(**kw) == bsa.BSA_ERR_INVALID
+
+
+def test_gate_norm_pointers():
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    L = bsa.lib()
+    assert L.bsa_gate_norm(None, None, None, None, None, None) == inv
+    assert _gn(dict(x=None)) == inv and _gn(h=None, z=None) == inv
+    assert _gn(dict(y=None, gate=None)) == inv                       # h without a branch
+    assert _gn(dict(y=None), h=None) == inv                          # a gate without a branch
+    assert _gn(z=None) == inv                                        # modulation of nothing
+    assert _gn(z_dtype=2) == inv and _gn(zs=A) == inv                # codes without scales, scales without codes
+    assert _gn(h=A, h_n=512, h_b=5120) == inv                        # on x, other strides
+    assert _gn(h=A + 512) == inv and _gn(h=A + BIG) == inv and _gn(z=A) == inv and _gn(z=A + 2 * BIG) == inv
+    assert _gn(dict(x=A + 1)) == al and _gn(dict(gate=A + 2)) == al and _gn(dict(pre_bias=A + 2)) == al
+    assert _gn(z_dtype=2, zs=A + 1) == al
+
+
+def _q8(x=A, codes=A + BIG, scale=A, **kw):
+    p = dict(B=1, N=10, S=4, L=128, x_dtype=0, x_b=0, x_n=128, x_s=1280, ld=512)
+    p.update(kw)
+    return bsa.lib().bsa_quantize_int8(ctypes.byref(bsa.bsa_quantize_int8_params(**p)), x, codes, scale, None)
+
+
+def test_quantize_int8_refusals():
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    for kw in (dict(B=0), dict(N=0), dict(S=0), dict(L=0), dict(S=257), dict(x_dtype=2), dict(ld=511), dict(x_s=-1),
+               dict(B=1 << 16, N=1 << 16, x_b=1280)):
+        assert _q8(**kw) == inv, kw
+    assert _q8(x=None) == inv and _q8(codes=None) == inv and _q8(scale=None) == inv
+    assert _q8(codes=A) == inv and _q8(codes=A + 1000) == inv        # over the rows that are read
+    assert _q8(x=A + 1) == al and _q8(scale=A + 2) == al
+
+
+def _lin(a=A, asc=A, w=A + BIG, wsc=A, bias=None, out=A + 2 * BIG, **kw):
+    p = dict(M=100, N=200, K=300, out_dtype=0, lda=304, ldw=304, ldo=200)
+    p.update(kw)
+    return bsa.lib().bsa_linear_int8(ctypes.byref(bsa.bsa_linear_int8_params(**p)), a, asc, w, wsc, bias, out, None)
+
+
+def test_linear_int8_refusals():
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    for kw in (dict(M=0), dict(N=0), dict(K=0), dict(K=32769, lda=32784, ldw=32784), dict(out_dtype=2), dict(lda=299), dict(ldw=288),
+               dict(ldo=199), dict(lda=-304)):
+        assert _lin(**kw) == inv, kw
+    for kw in (dict(a=None), dict(asc=None), dict(w=None), dict(wsc=None), dict(out=None), dict(out=A), dict(out=A + BIG + 64)):
+        assert _lin(**kw) == inv, kw
+    for kw in (dict(a=A + 8), dict(w=A + BIG + 1), dict(lda=301), dict(ldw=312), dict(out=A + 2 * BIG + 1), dict(asc=A + 2), dict(bias=A + 2)):
+        assert _lin(**kw) == al, kw
+
+
+def test_wrappers_refuse_tensors_that_are_not_on_a_device():
+    x = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    for call in (lambda: bsa.gate_norm(x), lambda: bsa.quantize_int8(x[0]),
+                 lambda: bsa.linear_int8(x[0].to(torch.int8), torch.ones(2), x[0].to(torch.int8), torch.ones(2)),
+                 lambda: bsa.rotary(x[:, None], None, None, torch.zeros(2, 1, dtype=torch.int32), torch.ones(64, dtype=torch.float64))):
+        with pytest.raises(bsa.BsaError) as e:
+            call()
+        assert e.value.status == bsa.BSA_ERR_INVALID

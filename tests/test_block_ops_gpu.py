@@ -1,0 +1,424 @@
+"""The operators around the attention on the GPU against the fp64 oracle.
+
+Tolerances, fixed before the first run.  u = 2^-24 is fp32's rounding, h the output type's half step
+(2^-8 bf16, 2^-24 fp32, relative to the value).
+  rotary   a value is two products and a sum of inputs of the pair; cos and sin (sincospif) are right to
+           about 2 u and their argument to u pi; the norm's square sum of 128 positive terms in a tree of
+           depth 8 + 4 and one rsqrt (2 u) give at most 10 u relative.  In all below 2^-20 (|x0| + |x1|) m.
+  gate     a sum of C values in chunks of 32 a thread, 5 steps in a warp and up to 32 warps is right to
+           70 u of the sum of magnitudes (2^-17.8); a mean square has only positive terms, so the
+           factor rsqrt is right to 2^-18; a layer norm's mean is right to 2^-17.8 mean |v|.
+  int8     codes and scales are bit-exact (one fp32 division, one product, one rounding); through the
+           fused norm a value moves by 2^-17 of the row's largest, so a code is within half a step + that.
+  linear   the sum is exact; its conversion, two products and a sum round 4 times: 4 u.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_video_bsa_b200 import bsa
+from oracle import bsa_oracle_block as orb
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+def rnd(seed, *shape, dtype=torch.float32, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def host(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ rotary
+
+def check_rotary(got, x, pos, freqs, layout, pairs, weight, eps, scale, inverse=False):
+    """got, x [B, H, N, 128] tensors; pos [B or 1, N, axes]."""
+    for b in range(x.shape[0]):
+        p = host(pos[b if pos.shape[0] > 1 else 0]).astype(np.int64)
+        ref = orb.rotary(host(x[b]), p, freqs.cpu().numpy(), layout, pairs, host(weight), eps, scale, inverse)
+        src = host(x[b]) if weight is None else orb.rms(host(x[b]), eps) * host(weight)
+        r = 2 * len(freqs)
+        size = np.abs(src)
+        part = size.copy()
+        lo = np.arange(r // 2) if layout == "half" else 2 * np.arange(r // 2)
+        hi = lo + (r // 2 if layout == "half" else 1)
+        part[..., lo] = part[..., hi] = scale * (size[..., lo] + size[..., hi])
+        tol = HALF[got.dtype] * np.abs(ref) + 2.0 ** -20 * part
+        err = np.abs(host(got[b]) - ref)
+        assert (err <= tol).all(), (err - tol).max()
+
+
+CASES = [
+    # B, H, N, r, layout, pairs, norm, in, out
+    (1, 1, 1, 128, "half", [64], False, torch.bfloat16, torch.bfloat16),
+    (1, 56, 1, 128, "interleaved", [64], True, torch.bfloat16, torch.bfloat16),
+    (2, 3, 17, 96, "half", [16, 16, 16], True, torch.bfloat16, torch.bfloat16),
+    (1, 5, 131, 96, "interleaved", [16, 16, 16], False, torch.float32, torch.float32),
+    (3, 2, 40, 10, "half", [5], True, torch.bfloat16, torch.float32),
+    (1, 17, 33, 2, "interleaved", [1], False, torch.float32, torch.bfloat16),
+    (1, 4, 9, 120, "half", [20, 20, 20], False, torch.bfloat16, torch.bfloat16),
+    (2, 2, 65, 32, "half", [4, 4, 4, 4], True, torch.float32, torch.float32),
+    (1, 7, 300, 128, "half", [22, 21, 21], True, torch.bfloat16, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("B,H,N,r,layout,pairs,norm,tin,tout", CASES)
+def test_rotary_from_a_token_major_projection(cuda_dev, B, H, N, r, layout, pairs, norm, tin, tout):
+    qkv = rnd(1, B, N, 3, H, 128, dtype=tin)
+    q, k, v = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pos = torch.randint(-1000, 1_000_000, (B, N, len(pairs)), generator=g, device="cuda", dtype=torch.int32)
+    freqs, m = bsa.rotary_freqs(pairs, scaling="yarn", factor=4.0, trained_length=4096)
+    wq, wk = (1 + rnd(3 + i, 128, scale=0.1) if norm else None for i in range(2))
+    keep = qkv.clone()
+    Q, K, V = bsa.rotary(q, k, v, pos, freqs, layout, pairs, wq, wk, 1e-6, m, out_dtype=tout)
+    assert Q.shape == (B, H, N, 128) and Q.is_contiguous() and Q.dtype == tout
+    check_rotary(Q, q, pos, freqs, layout, pairs, wq, 1e-6, m)
+    check_rotary(K, k, pos, freqs, layout, pairs, wk, 1e-6, m)
+    assert torch.equal(V, v.to(tout))
+    assert torch.equal(qkv, keep)
+
+
+def test_rotary_far_positions(cuda_dev):
+    # the ends of int32, where fp32 angles would be off by whole turns
+    N = 6
+    pos = torch.tensor([[2 ** 31 - 1], [-2 ** 31], [2 ** 30 + 7], [1], [0], [-1]], dtype=torch.int32, device="cuda")
+    q = rnd(5, 1, 2, N, 128)
+    freqs, m = bsa.rotary_freqs(64)
+    Q, _, _ = bsa.rotary(q, None, None, pos, freqs)
+    # fp64 keeps f to 2^-53: 2^31 of it is 2^-22 of a radian
+    ref = orb.rotary(host(q[0]), host(pos).astype(np.int64), freqs.cpu().numpy(), "half", [64])
+    assert np.abs(host(Q[0]) - ref).max() <= (2.0 ** -20 + 2.0 ** -21) * 2 * np.abs(host(q)).max()
+
+
+def test_rotary_in_place_and_inverse(cuda_dev):
+    B, H, N = 2, 4, 50
+    qkv = rnd(6, B, N, 3, H, 128)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    freqs, _ = bsa.rotary_freqs(48)
+    views = [qkv[:, :, i].transpose(1, 2) for i in range(3)]
+    Q, K, V = bsa.rotary(*views, pos, freqs)
+    keep = qkv.clone()
+    a = bsa.rotary(*views, pos, freqs, out=views)
+    assert a[0].data_ptr() == views[0].data_ptr()
+    assert torch.equal(views[0], Q) and torch.equal(views[1], K) and torch.equal(views[2], V)
+    back = bsa.rotary(*views, pos, freqs, inverse=True)
+    for i in range(3):
+        want = keep[:, :, i].transpose(1, 2)
+        assert (back[i] - want).abs().max() <= 2.0 ** -19 * 2 * want.abs().max()
+
+
+def test_rotary_leaves_the_rest_alone(cuda_dev):
+    # outputs inside a larger buffer: nothing around them is written; NaN and infinity past rotary_dim pass
+    B, H, N = 1, 3, 21
+    big = torch.full((B, H, N + 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = rnd(7, B, H, N, 128, dtype=torch.bfloat16)
+    q[..., 100] = float("inf")
+    q[..., 127] = float("nan")
+    out = big[:, :, 2:2 + N]
+    freqs, _ = bsa.rotary_freqs(25)
+    for layout in ("half", "interleaved"):
+        big.fill_(7.0)
+        bsa.rotary(q, None, None, torch.arange(N, dtype=torch.int32, device="cuda"), freqs, layout, out=[out, None, None])
+        assert (big[:, :, :2] == 7).all() and (big[:, :, 2 + N:] == 7).all()
+        assert torch.equal(out[..., 50:127], q[..., 50:127]) and out[..., 127].isnan().all()
+        assert out[..., :50].isfinite().all()
+
+
+def test_rotary_other_head_counts_and_streams(cuda_dev):
+    q, k, v = rnd(8, 1, 8, 30, 128), rnd(9, 1, 2, 30, 128), rnd(10, 1, 2, 30, 128)
+    pos = torch.arange(30, dtype=torch.int32, device="cuda")
+    freqs, _ = bsa.rotary_freqs(64)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    Q, K, V = bsa.rotary(q, k, v, pos, freqs, stream=s)
+    s.synchronize()
+    check_rotary(Q, q, pos[None, :, None], freqs, "half", [64], None, 0, 1.0)
+    check_rotary(K, k, pos[None, :, None], freqs, "half", [64], None, 0, 1.0)
+    assert torch.equal(V, v)
+
+
+# ------------------------------------------------------------------ gate norm
+
+def run_gate_norm(x, y, gate, scale, shift, pre, post, aff, eps, rs=1.0, bs=1.0, **kw):
+    C = x.shape[-1]
+    ws = [1 + rnd(40 + i, C, scale=0.1) if i % 2 == 0 else rnd(40 + i, C, scale=0.1) for i in range(4)] if aff else [None] * 4
+    if y is None:
+        ws[2] = ws[3] = None
+    h, z = bsa.gate_norm(x, y, gate, scale, shift, pre, ws[0], ws[1], post, ws[2], ws[3], eps, rs, bs, **kw)
+    return h, z, ws
+
+
+def gate_norm_bounds(x, y, gate, scale, shift, pre, post, ws, eps, rs, bs):
+    """(h, z, error bound of h, error bound of z) before the output's rounding, from the formulas."""
+    full = lambda t: None if t is None else host(t if t.dim() == 3 else (t[:, None] if t.dim() == 2 else t[None, None]))  # noqa: E731
+    X, Y, G, S, T = host(x), host(y), full(gate), full(scale), full(shift)
+    W = [host(w) for w in ws]
+    h, z = orb.gate_norm(X, Y, G, S, T, pre, W[0], W[1], post, W[2], W[3], eps, rs, bs)
+
+    def norm_err(v, e, kind, w, b):
+        """Bound of norm(v) when v is off by e: (value, bound)."""
+        if kind == "none":
+            n, f = v, e
+        else:
+            c = v - v.mean(-1, keepdims=True) if kind == "layer" else v
+            inv = 1.0 / np.sqrt((c * c).mean(-1, keepdims=True) + eps)
+            # the mean's own error, then the factor's: rms(e) moves the deviation's root by at most itself
+            em = 2.0 ** -17.8 * np.abs(v).mean(-1, keepdims=True) + e.mean(-1, keepdims=True) if kind == "layer" else 0.0
+            ee = e + em
+            rel = 2.0 ** -18 + np.sqrt((ee * ee).mean(-1, keepdims=True)) * inv
+            n, f = c * inv, ee * inv + np.abs(c * inv) * rel
+        if w is not None:
+            n, f = n * w, f * np.abs(w) + 2.0 ** -23 * np.abs(n * w)
+        if b is not None:
+            n, f = n + b, f + 2.0 ** -23 * np.abs(n + b)
+        return n, f
+    eh = np.zeros_like(X)
+    if Y is not None:
+        n, f = norm_err(Y, np.zeros_like(Y), post, W[2], W[3])
+        g = 1.0 if G is None else G
+        eh = np.abs(bs * g) * (f + 2.0 ** -22 * np.abs(n)) + 2.0 ** -23 * (np.abs(rs * X) + np.abs(h))
+    n, f = norm_err(h, eh, pre, W[0], W[1])
+    a = 1.0 if S is None else 1.0 + S
+    ez = np.abs(a) * (f + 2.0 ** -22 * np.abs(n)) + 2.0 ** -23 * np.abs(n) + 2.0 ** -23 * np.abs(z)
+    return h, z, eh, ez
+
+
+def close(got, want, bound):
+    err = np.abs(host(got) - want)
+    tol = bound + HALF[got.dtype] * np.abs(want) + 1e-37
+    assert (err <= tol).all(), ((err - tol).max(), np.unravel_index((err - tol).argmax(), err.shape))
+
+
+GN = [
+    # B, N, C, pre, post, x, y, mod, mod shape, affine
+    (1, 1, 7168, "rms", "rms", torch.bfloat16, torch.bfloat16, torch.float32, "b", True),
+    (2, 5, 256, "layer", "rms", torch.bfloat16, torch.bfloat16, torch.bfloat16, "b1", False),
+    (3, 7, 1111, "layer", "layer", torch.float32, torch.bfloat16, torch.bfloat16, "n", True),
+    (1, 400, 512, "rms", "none", torch.float32, torch.float32, torch.float32, "n", True),
+    (2, 300, 1000, "none", "layer", torch.bfloat16, torch.float32, torch.float32, "c", True),
+    (1, 3, 1, "rms", "layer", torch.float32, torch.float32, torch.float32, "b", False),
+    (1, 2, 7, "layer", "rms", torch.bfloat16, torch.bfloat16, torch.float32, "b", True),
+    (1, 310, 7168, "layer", "rms", torch.bfloat16, torch.bfloat16, torch.float32, "b", False),
+    (1, 301, 8200, "rms", "rms", torch.bfloat16, torch.bfloat16, torch.bfloat16, "b", False),
+    (1, 300, 16640, "layer", "rms", torch.float32, torch.bfloat16, torch.float32, "b", True),
+    (1, 2, 32768, "rms", "layer", torch.bfloat16, torch.bfloat16, torch.float32, "b", True),
+    (1, 2, 32767, "layer", "layer", torch.float32, torch.bfloat16, torch.float32, "b", False),
+]
+
+
+@pytest.mark.parametrize("B,N,C,pre,post,tx,ty,tm,shape,aff", GN)
+def test_gate_norm(cuda_dev, B, N, C, pre, post, tx, ty, tm, shape, aff):
+    x, y = rnd(11, B, N, C, dtype=tx) + 3, rnd(12, B, N, C, dtype=ty) + 1
+    s = dict(b=(B, C), b1=(B, 1, C), n=(B, N, C), c=(C,))[shape]
+    gate, scale, shift = (rnd(13 + i, *s, dtype=tm, scale=0.5) for i in range(3))
+    args = (x, y, gate, scale, shift, pre, post)
+    h, z, ws = run_gate_norm(*args, aff, 1e-6, 0.5, 2.0)
+    assert h.dtype == tx and z.dtype == torch.bfloat16
+    hr, zr, eh, ez = gate_norm_bounds(*args, ws, 1e-6, 0.5, 2.0)
+    close(h, hr, eh)
+    close(z, zr, ez)
+    # fp32 result, and the residual updated in place: the same values
+    x2 = x.clone()
+    h2, z2, _ = run_gate_norm(x2, *args[1:], aff, 1e-6, 0.5, 2.0, h_out=x2, z_dtype=torch.float32)
+    assert h2 is x2 and torch.equal(h2, h) and torch.equal(z2.bfloat16(), z)
+    close(z2, zr, ez)
+    # the two halves alone
+    h3, none, _ = run_gate_norm(x, y, gate, None, None, pre, post, False, 1e-6, want_z=False)
+    assert none is None and h3.shape == x.shape
+    same, z4, ws4 = run_gate_norm(x, None, None, scale, shift, pre, "none", aff, 1e-6)
+    assert same is x
+    _, zr4, _, ez4 = gate_norm_bounds(x, None, None, scale, shift, pre, "none", ws4, 1e-6, 1.0, 1.0)
+    close(z4, zr4, ez4)
+
+
+@pytest.mark.parametrize("C", [64, 1111, 7168])
+def test_gate_norm_codes(cuda_dev, C):
+    B, N = 2, 170
+    x, y = rnd(20, B, N, C, dtype=torch.bfloat16), rnd(21, B, N, C, dtype=torch.bfloat16)
+    gate, scale, shift = (rnd(22 + i, B, C, scale=0.5) for i in range(3))
+    args = (x, y, gate, scale, shift, "layer", "rms")
+    h, (codes, top), ws = run_gate_norm(*args, True, 1e-6, quantize=True)
+    _, zr, _, ez = gate_norm_bounds(*args, ws, 1e-6, 1.0, 1.0)
+    zr, ez = zr.reshape(B * N, C), ez.reshape(B * N, C)
+    amax = np.abs(zr).max(1)
+    assert codes.shape == (B * N, C) and codes.stride(0) % 16 == 0
+    assert (np.abs(host(top) - amax / 127) <= ez.max(1) / 127 + 2.0 ** -23 * amax / 127).all()
+    err = np.abs(host(codes) * host(top)[:, None] - zr)
+    assert (err <= 0.5 * host(top)[:, None] * (1 + 2.0 ** -16) + 2 * ez.max(1)[:, None]).all()
+    assert (codes.abs().amax(1) == 127).all()
+    # one source of truth: the codes of the fp32 result are the same codes
+    _, z32, _ = run_gate_norm(*args, True, 1e-6, z_dtype=torch.float32)
+    c2, t2 = bsa.quantize_int8(z32)
+    assert torch.equal(c2, codes) and torch.equal(t2, top)
+
+
+def test_gate_norm_odd_rows_and_strides(cuda_dev):
+    # rows inside wider buffers, at an odd offset: scalar accesses, nothing around them written
+    B, N, C = 2, 9, 130
+    wide = rnd(30, B, N, C + 7, dtype=torch.bfloat16)
+    x, y = wide[..., 3:3 + C], rnd(31, B, N, 2 * C)[..., 1:1 + C]
+    buf = torch.full((B, N, C + 6), 9.0, dtype=torch.bfloat16, device="cuda")
+    h, z = bsa.gate_norm(x, y, pre="rms", post="rms", h_out=buf[..., 3:3 + C])
+    hr, zr, eh, ez = gate_norm_bounds(x, y, None, None, None, "rms", "rms", [None] * 4, 1e-6, 1.0, 1.0)
+    close(h, hr, eh)
+    close(z, zr, ez)
+    assert (buf[..., :3] == 9).all() and (buf[..., 3 + C:] == 9).all()
+
+
+def test_gate_norm_extreme_rows(cuda_dev):
+    C = 512
+    x = rnd(32, 1, 6, C)
+    x[0, 0] = 0.0                      # nothing: eps keeps it 0
+    x[0, 1] = 5.0                      # no deviation: a layer norm gives 0
+    x[0, 2] *= 1e-20
+    x[0, 3, 7] = float("inf")
+    x[0, 4, 9] = float("nan")
+    x[0, 5] += 1e4                     # large mean, small deviation
+    for pre in ("rms", "layer"):
+        _, z = bsa.gate_norm(x, pre=pre, z_dtype=torch.float32)
+        rows = [0, 1, 2, 5]
+        _, zr, _, ez = gate_norm_bounds(x[:, rows], None, None, None, None, pre, "none", [None] * 4, 1e-6, 1.0, 1.0)
+        close(z[:, rows], zr, ez)
+        assert not z[0, 3].isfinite().all() and z[0, 4].isnan().all()
+        _, (codes, top) = bsa.gate_norm(x, pre=pre, quantize=True)
+        assert top[[3, 4]].isnan().all() and not codes[[3, 4]].any() and top[[0, 1, 2, 5]].isfinite().all()
+
+
+# ------------------------------------------------------------------ int8 rows and product
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 7168), (3, 17), (300, 7168), (400, 1111), (2, 32768), (299, 28672), (1, 32767), (500, 256)])
+def test_quantize_int8_is_bit_exact(cuda_dev, M, K, dtype):
+    x = rnd(50, M, K, dtype=dtype) * (1 + 9 * (rnd(51, K) > 2)).to(dtype)
+    codes, scale = bsa.quantize_int8(x)
+    c, s = orb.quantize_int8(x.float().cpu().numpy())
+    assert (codes.cpu().numpy() == c).all() and (scale.cpu().numpy() == s).all()
+
+
+def test_quantize_int8_rows_of_special_values(cuda_dev):
+    x = rnd(52, 8, 100, dtype=torch.bfloat16)
+    x[0] = 0
+    x[1, 3] = float("inf")
+    x[2, 99] = float("nan")
+    x[3] *= 1e-37
+    x[4] = 3e38
+    x[5, 0] = -float("inf")
+    codes, scale = bsa.quantize_int8(x)
+    c, s = orb.quantize_int8(x.float().cpu().numpy())
+    assert (codes.cpu().numpy() == c).all() and np.array_equal(scale.cpu().numpy(), s, equal_nan=True)
+
+
+@pytest.mark.parametrize("B,H,N", [(1, 56, 130), (2, 3, 33), (1, 1, 1)])
+def test_quantize_int8_of_head_major_rows(cuda_dev, B, H, N):
+    O = rnd(53, B, H, N, 128, dtype=torch.bfloat16)
+    codes, scale = bsa.quantize_int8(O)
+    flat = O.permute(0, 2, 1, 3).reshape(B * N, H * 128)
+    c, s = bsa.quantize_int8(flat)
+    assert torch.equal(codes, c) and torch.equal(scale, s)
+    odd = rnd(54, B, H, N, 129)[..., 1:]          # rows that start on no boundary, a segment of 128
+    c, s = bsa.quantize_int8(odd)
+    c2, s2 = bsa.quantize_int8(odd.permute(0, 2, 1, 3).reshape(B * N, H * 128))
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+
+
+def codes_of(seed, M, K):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    buf = torch.full((M, -(-K // 16) * 16), 77, dtype=torch.int8, device="cuda")   # what lies past K must not count
+    buf[:, :K] = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    return buf[:, :K]
+
+
+SHAPES = [(1, 1, 1), (1, 128, 128), (1, 7168, 7168), (3, 200, 300), (16, 129, 1111), (17, 256, 128), (33, 515, 1111), (64, 1000, 515),
+          (65, 130, 640), (127, 128, 4096), (128, 128, 128), (129, 257, 129), (255, 512, 1000), (256, 256, 256), (257, 513, 16), (300, 40, 7168),
+          (513, 1030, 2049), (1000, 515, 1111), (1500, 2304, 900), (2, 21504, 640), (40, 7168, 28672), (700, 16, 32768)]
+
+
+def check_linear(M, N, K, out_dtype, bias, seed=60, out=None):
+    a, w = codes_of(seed, M, K), codes_of(seed + 1, N, K)
+    sa, sw = rnd(seed + 2, M).abs() + 0.01, rnd(seed + 3, N).abs() + 0.01
+    b = rnd(seed + 4, N, scale=100.0) if bias else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = bsa.linear_int8(a, sa, w, sw, b, out_dtype, out, status)
+    # the whole sum in fp64: products of at most 127^2, fewer than 2^15 of them, are exact
+    total = (a.double() @ w.double().t()) * sa.double()[:, None] * sw.double()
+    ref = total if b is None else total + b.double()
+    tol = HALF[got.dtype] * ref.abs() + 4 * 2.0 ** -24 * (total.abs() + (0 if b is None else b.double().abs()))
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), (err - tol).max().item()
+    assert int(status) == 0
+    return got
+
+
+@pytest.mark.parametrize("out_dtype,bias", [(torch.bfloat16, True), (torch.float32, False)])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_int8(cuda_dev, M, N, K, out_dtype, bias):
+    check_linear(M, N, K, out_dtype, bias)
+
+
+def test_linear_int8_rows_of_a_wider_output(cuda_dev):
+    for M, N, K in ((5, 77, 100), (300, 130, 200), (600, 333, 64)):
+        for dtype in (torch.bfloat16, torch.float32):
+            buf = torch.full((M + 2, N + 9), 5.0, dtype=dtype, device="cuda")
+            check_linear(M, N, K, dtype, True, out=buf[1:1 + M, 4:4 + N])
+            assert (buf[0] == 5).all() and (buf[-1] == 5).all() and (buf[:, :4] == 5).all() and (buf[:, 4 + N:] == 5).all()
+
+
+def test_linear_int8_largest_sums(cuda_dev):
+    # every product 127^2 of the longest rows: 2^15 127^2 < 2^31 stays exact
+    for M in (2, 300):
+        a = torch.full((M, 32768), 127, dtype=torch.int8, device="cuda")
+        w = torch.full((40, 32768), -127, dtype=torch.int8, device="cuda")
+        one = torch.ones(300, device="cuda")
+        out = bsa.linear_int8(a, one[:M], w, one[:40], out_dtype=torch.float32)
+        assert (out == float(np.float32(-127 * 127 * 32768))).all()
+
+
+def test_linear_int8_marks_rows_without_a_scale(cuda_dev):
+    x = rnd(70, 40, 256)
+    x[7, 3] = float("nan")
+    a, sa = bsa.quantize_int8(x)
+    w, sw = bsa.quantize_int8(rnd(71, 30, 256))
+    out = bsa.linear_int8(a, sa, w, sw)
+    assert out[7].isnan().all() and out[:7].isfinite().all() and out[8:].isfinite().all()
+
+
+# ------------------------------------------------------------------ together, and as graphs
+
+def test_calls_are_deterministic_and_captured(cuda_dev):
+    B, N, H, C = 1, 200, 4, 512
+    x, y = rnd(80, B, N, C, dtype=torch.bfloat16), rnd(81, B, N, C, dtype=torch.bfloat16)
+    gate, scale, shift = (rnd(82 + i, B, C) for i in range(3))
+    w, sw = bsa.quantize_int8(rnd(85, 3 * H * 128, C))
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    freqs, m = bsa.rotary_freqs(64)
+    one = 1 + rnd(86, 128, scale=0.1)
+
+    def step():
+        h, (a, sa) = bsa.gate_norm(x, y, gate, scale, shift, post="rms", quantize=True)
+        qkv = bsa.linear_int8(a, sa, w, sw).view(B, N, 3, H, 128)
+        Q, K, V = bsa.rotary(*(qkv[:, :, i].transpose(1, 2) for i in range(3)), pos, freqs, q_weight=one, k_weight=one)
+        O = bsa.forward(Q, K, V, 1)
+        return (h, Q, K, V, O, *bsa.quantize_int8(O))
+
+    first = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = step()
+        graphs.append((g, outs))
+    for g, outs in graphs:
+        g.replay()
+    for g, outs in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for g, outs in graphs:
+        for a, b in zip(first, outs):
+            assert torch.equal(a, b)
