@@ -9,6 +9,7 @@ device is not sm_100 the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -71,7 +72,7 @@ class bsa_gate_norm_params(ctypes.Structure):
                 + [(n, _f32) for n in ("eps", "residual_scale", "branch_scale")]
                 + [(n, _i64) for n in ("x_b", "x_n", "y_b", "y_n", "h_b", "h_n", "z_b", "z_n",
                                        "gate_b", "gate_n", "scale_b", "scale_n", "shift_b",
-                                       "shift_n")])
+                                       "shift_n")] + [("dev_status", ctypes.c_void_p)])
 
 
 class bsa_gate_norm_inputs(ctypes.Structure):
@@ -522,37 +523,57 @@ def bsa_debug_expired_wait(dev_status, timeout_ns: int, stream=None):
 
 
 # --------------------------------------------------------------- around the attention
+#
+# A call on one token is a few microseconds on the GPU, so these wrappers keep
+# the host's share small: checks of shapes, strides and types and the filled
+# parameter struct are a pure function of the arguments' layout and are kept
+# per layout (never per address); a repeated layout costs a lookup, the output
+# allocations and the launch.
 
 def _need(ok, where):
     if not ok:
         raise BsaError(BSA_ERR_INVALID, where)
 
 
-def _run(ref, stream, where, call):
-    """call(stream pointer) with ref's device current; its outputs belong to the stream."""
+def _sig(t):
+    """What a plan may depend on: a tensor's layout, never its address."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+
+
+def _one_device(where, ref, *sigs):
+    """The CUDA device of every given tensor."""
+    _need(ref[3] >= 0, where)
+    for g in sigs:
+        _need(g is None or g[3] == ref[3], where)
+    return ref[3]
+
+
+def _elsewhere(device, stream, where):
+    """Context in which `device` is current and outputs belong to `stream`."""
     if stream is None:
-        if ref.device.index == torch.cuda.current_device():
-            return call(_stream())
-        with torch.cuda.device(ref.device):
-            return call(_stream())
-    _need(stream.device == ref.device, where)
-    with torch.cuda.stream(stream):
-        return call(_stream(stream))
+        return torch.cuda.device(device)
+    _need(stream.device.index == device, where)
+    return torch.cuda.stream(stream)
 
 
-def _same_device(where, ref, *tensors):
-    _need(ref.is_cuda, where)
-    for t in tensors:
-        _need(t is None or t.device == ref.device, where)
+def _here(device, stream):
+    return stream is None and torch._C._cuda_getDevice() == device
 
 
-def _vector(t, n, where):
-    """An fp32 vector of n values, contiguous, or None."""
-    _need(t is None or (t.dtype == torch.float32 and t.shape == (n,) and t.is_contiguous()), where)
+def _vector(g, n, where):
+    """An fp32 vector of n contiguous values, or None."""
+    _need(g is None or (g[0] is torch.float32 and g[1] == (n,) and (n == 1 or g[2] == (1,))), where)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
 
 
 def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_length=0,
@@ -571,19 +592,51 @@ def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_lengt
     return torch.tensor(out, dtype=torch.float64, device=device), scale.value
 
 
-def _rotary_call(parts, weights, outs, positions, freqs, layout, axis_pairs, eps, scale, inverse,
-                 stream):
-    ref, o = next((x, y) for x, y in zip(parts, outs) if x is not None)
-    B, H, N, D = ref.shape
-    p = bsa_rotary_params(B, H, N, D, 2 * freqs.numel(), ROPE_LAYOUTS[layout], len(axis_pairs),
-                          (_i32 * 4)(*axis_pairs), int(inverse), DTYPES[ref.dtype],
-                          DTYPES[o.dtype], scale, eps, ref.stride(0), ref.stride(1), ref.stride(2),
-                          o.stride(0), o.stride(1), o.stride(2),
-                          positions.stride(0) if positions.dim() == 3 and positions.shape[0] > 1
-                          else 0, positions.stride(-2))
-    _check(lib().bsa_rotary(ctypes.byref(p), *[_addr(x) for x in parts], _addr(positions),
-                            _addr(freqs), *[_addr(w) for w in weights], *[_addr(y) for y in outs],
-                            stream), "bsa_rotary")
+@functools.lru_cache(maxsize=256)
+def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inverse, out_dtype):
+    """(device, output shapes and types, launches): a launch is the filled struct and the indices of
+    the tensors it takes (those that share their layout)."""
+    where = "rotary"
+    given = [g for g in parts if g is not None]
+    _need(given and len(outs) == 3 and pos is not None and fr is not None, where)
+    device = _one_device(where, given[0], *given, *outs, pos, fr, *weights)
+    B, N = given[0][1][0], given[0][1][2]
+    for dtype, shape, stride, _ in given:
+        _need(dtype in _FLOATS and len(shape) == 4 and shape[0] == B and shape[2] == N
+              and shape[3] == 128 and stride[3] == 1, where)
+    _need(fr[0] is torch.float64 and len(fr[1]) == 1 and (fr[1][0] <= 1 or fr[2] == (1,)), where)
+    pairs = (fr[1][0],) if pairs is None else pairs
+    _need(1 <= len(pairs) <= 4 and sum(pairs) == fr[1][0], where)
+    pdtype, pshape, pstride, _ = pos
+    if len(pshape) == 1:
+        pshape, pstride = (*pshape, 1), (*pstride, 1)
+    _need(pdtype is torch.int32 and len(pshape) in (2, 3) and pshape[-2:] == (N, len(pairs))
+          and (pshape[-1] == 1 or pstride[-1] == 1)
+          and (len(pshape) == 2 or pshape[0] in (1, B)), where)
+    pos_b = pstride[0] if len(pshape) == 3 and pshape[0] > 1 else 0
+    for g in weights:
+        _vector(g, 128, where)
+    want, kinds = [], {}
+    for i, (x, y) in enumerate(zip(parts, outs)):
+        if x is None:
+            _need(y is None, where)
+            want.append(None)
+            continue
+        dtype, shape, stride, _ = x
+        H = shape[1]
+        if y is None:
+            y = (out_dtype or dtype, shape, (H * N * 128, N * 128, 128, 1), device)
+        _need(y[0] in _FLOATS and y[1] == shape and y[2][3] == 1, where)
+        want.append((y[1], y[0]))
+        kinds.setdefault((H, stride, dtype, y[2], y[0]), []).append(i)
+    launches = []
+    for (H, stride, dtype, ostride, odtype), ids in kinds.items():
+        p = bsa_rotary_params(B, H, N, 128, 2 * fr[1][0], ROPE_LAYOUTS[layout], len(pairs),
+                              (_i32 * 4)(*pairs), int(inverse), DTYPES[dtype], DTYPES[odtype],
+                              scale, eps, stride[0], stride[1], stride[2], ostride[0], ostride[1],
+                              ostride[2], pos_b, pstride[-2])
+        launches.append((ctypes.byref(p), tuple(ids)))
+    return device, tuple(want), tuple(launches)
 
 
 def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=None, k_weight=None,
@@ -594,60 +647,69 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
     Any of q, k, v may be None.  positions int32 [N, axes] or [B, N, axes] ([N] for one axis),
     freqs fp64 [pairs] from ``rotary_freqs``; axis_pairs lists the pairs of each axis.  k and v may
     have another head count than q.  ``out`` gives the outputs (a tensor may be its own output)."""
-    where = "rotary"
-    parts = [q, k, v]
-    given = [x for x in parts if x is not None]
-    _need(given, where)
-    ref = given[0]
-    _same_device(where, ref, *given, positions, freqs, q_weight, k_weight)
-    B, N, axis_pairs = ref.shape[0], ref.shape[2], list(axis_pairs or [freqs.numel()])
-    for x in given:
-        _need(x.dim() == 4 and x.dtype in (torch.bfloat16, torch.float32) and x.shape[0] == B
-              and x.shape[2] == N and x.shape[3] == 128 and x.stride(3) == 1, where)
-    if positions.dim() == 1:
-        positions = positions[:, None]
-    _need(positions.dtype == torch.int32 and positions.dim() in (2, 3)
-          and positions.shape[-2:] == (N, len(axis_pairs)) and positions.stride(-1) == 1
-          and (positions.dim() == 2 or positions.shape[0] in (1, B)), where)
-    _need(freqs.dtype == torch.float64 and freqs.dim() == 1 and freqs.is_contiguous()
-          and len(axis_pairs) <= 4, where)
-    weights = [q_weight, k_weight]
-    for w in weights:
-        _vector(w, 128, where)
-
-    def call(st):
-        outs = list(out) if out is not None else [
-            None if x is None else torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-            for x in parts]
-        _need(len(outs) == 3, where)
-        for x, y in zip(parts, outs):
-            _need((x is None) == (y is None), where)
-            _need(y is None or (y.shape == x.shape and y.device == x.device and y.stride(3) == 1
-                                and y.dtype in (torch.bfloat16, torch.float32)), where)
-        # one launch for the tensors that share their layout
-        kinds = {}
-        for i, (x, y) in enumerate(zip(parts, outs)):
-            if x is not None:
-                kinds.setdefault((x.shape, x.stride(), x.dtype, y.stride(), y.dtype), []).append(i)
-        for ids in kinds.values():
-            pick = lambda t: [t[i] if i in ids else None for i in range(len(t))]  # noqa: E731
-            _rotary_call(pick(parts), pick(weights), pick(outs), positions, freqs, layout,
-                         axis_pairs, eps, scale, inverse, st)
-        return tuple(outs)
-
-    return _run(ref, stream, where, call)
+    outs = out if out is not None else (None, None, None)
+    device, want, launches = _rotary_plan(
+        (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions), _sig(freqs),
+        (_sig(q_weight), _sig(k_weight)), layout,
+        None if axis_pairs is None else tuple(axis_pairs), eps, scale, bool(inverse), out_dtype)
+    if not _here(device, stream):
+        with _elsewhere(device, stream, "rotary"):
+            return rotary(q, k, v, positions, freqs, layout, axis_pairs, q_weight, k_weight, eps,
+                          scale, inverse, out, out_dtype)
+    outs = [w if w is None else (y if y is not None else
+                                 torch.empty(w[0], dtype=w[1], device=freqs.device))
+            for w, y in zip(want, outs)]
+    qkv, weights, st = (q, k, v), (q_weight, k_weight, None), _raw_stream(device)
+    for p, ids in launches:
+        a, w, o = [None] * 3, [None] * 3, [None] * 3
+        for i in ids:
+            a[i], w[i], o[i] = qkv[i].data_ptr(), _addr(weights[i]), outs[i].data_ptr()
+        _check(lib().bsa_rotary(p, *a, positions.data_ptr(), freqs.data_ptr(), w[0], w[1], *o, st),
+               "bsa_rotary")
+    return tuple(outs)
 
 
-def _mod(t, B, N, C, where):
+def _mod(g, B, N, C, where):
     """(batch stride, token stride) of a vector [C], [B or 1, C] or [B or 1, N or 1, C]."""
-    if t is None:
+    if g is None:
         return 0, 0
-    _need(t.shape[-1] == C and t.stride(-1) == 1 and t.dim() <= 3, where)
-    if t.dim() == 1:
+    _, shape, stride, _ = g
+    _need(1 <= len(shape) <= 3 and shape[-1] == C and (C == 1 or stride[-1] == 1), where)
+    if len(shape) == 1:
         return 0, 0
-    _need(t.shape[0] in (1, B) and (t.dim() == 2 or t.shape[1] in (1, N)), where)
-    return (t.stride(0) if t.shape[0] > 1 else 0,
-            t.stride(1) if t.dim() == 3 and t.shape[1] > 1 else 0)
+    _need(shape[0] in (1, B) and (len(shape) == 2 or shape[1] in (1, N)), where)
+    return (stride[0] if shape[0] > 1 else 0,
+            stride[1] if len(shape) == 3 and shape[1] > 1 else 0)
+
+
+def _rows(g, C):
+    """Strides (batch, token) of rows [B, N, C]."""
+    return (0, 0) if g is None else (g[2][0], g[2][1])
+
+
+@functools.lru_cache(maxsize=256)
+def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, residual_scale,
+                    branch_scale, quantize, z_dtype, want_z):
+    where = "gate_norm"
+    device = _one_device(where, x, y, gate, scale, shift, *vectors, h_out)
+    _need(len(x[1]) == 3 and pre in NORMS and post in NORMS and z_dtype in _FLOATS, where)
+    B, N, C = x[1]
+    for g in (x, y, h_out):
+        _need(g is None or (g[0] in _FLOATS and g[1] == x[1] and (C == 1 or g[2][2] == 1)), where)
+    _need(h_out is None or (y is not None and h_out[0] is x[0]), where)
+    mods = [g[0] for g in (gate, scale, shift) if g is not None]
+    for dtype in mods:
+        _need(dtype in _FLOATS and dtype is mods[0], where)
+    for g in vectors:
+        _vector(g, C, where)
+    ld = -(-C // 16) * 16 if quantize else C
+    h = (N * C, C) if h_out is None else _rows(h_out, C)
+    p = bsa_gate_norm_params(
+        B, N, C, NORMS[pre], NORMS[post], DTYPES[x[0]], DTYPES[y[0]] if y else 0,
+        DTYPES[mods[0]] if mods else 1, 2 if quantize and want_z else DTYPES[z_dtype], eps,
+        residual_scale, branch_scale, *_rows(x, C), *_rows(y, C), *h, N * ld, ld,
+        *_mod(gate, B, N, C, where), *_mod(scale, B, N, C, where), *_mod(shift, B, N, C, where))
+    return device, ctypes.byref(p), x[1], B * N, C, ld
 
 
 def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weight=None,
@@ -660,107 +722,98 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     x, y [B, N, C]; gate, scale, shift [C], [B, C], [B, 1, C] or [B, N, C]; weights and biases fp32
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
-    where = "gate_norm"
-    _same_device(where, x, y, gate, scale, shift, pre_weight, pre_bias, post_weight, post_bias,
-                 h_out)
-    _need(x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32) and x.stride(2) == 1, where)
-    B, N, C = x.shape
-    _need(y is None or (y.shape == x.shape and y.stride(2) == 1
-                        and y.dtype in (torch.bfloat16, torch.float32)), where)
-    _need(h_out is None or (y is not None and h_out.shape == x.shape and h_out.dtype == x.dtype
-                            and h_out.stride(2) == 1), where)
-    _need(z_dtype in (torch.bfloat16, torch.float32) and pre in NORMS and post in NORMS, where)
-    mods = [t for t in (gate, scale, shift) if t is not None]
-    mod_dtype = mods[0].dtype if mods else torch.float32
-    for t in mods:
-        _need(t.dtype == mod_dtype and t.dtype in (torch.bfloat16, torch.float32), where)
-    for w in (pre_weight, pre_bias, post_weight, post_bias):
-        _vector(w, C, where)
-    gs, ss, hs = (_mod(t, B, N, C, where) for t in (gate, scale, shift))
+    device, p, shape, rows, C, ld = _gate_norm_plan(
+        _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
+        (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out), pre,
+        post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z)
+    if not _here(device, stream):
+        with _elsewhere(device, stream, "gate_norm"):
+            return gate_norm(x, y, gate, scale, shift, pre, pre_weight, pre_bias, post, post_weight,
+                             post_bias, eps, residual_scale, branch_scale, quantize, z_dtype, h_out,
+                             want_z)
+    h, z, zs = h_out, None, None
+    if h is None and y is not None:
+        h = torch.empty(shape, dtype=x.dtype, device=x.device)
+    if want_z and quantize:
+        z = torch.empty((rows, ld), dtype=torch.int8, device=x.device)
+        zs = torch.empty(rows, dtype=torch.float32, device=x.device)
+    elif want_z:
+        z = torch.empty(shape, dtype=z_dtype, device=x.device)
+    i = bsa_gate_norm_inputs(x.data_ptr(), _addr(y), _addr(gate), _addr(scale), _addr(shift),
+                             _addr(post_weight), _addr(post_bias), _addr(pre_weight),
+                             _addr(pre_bias))
+    _check(lib().bsa_gate_norm(p, ctypes.byref(i), _addr(h), _addr(z), _addr(zs),
+                               _raw_stream(device)), "bsa_gate_norm")
+    if zs is not None:
+        z = (z if ld == C else z[:, :C], zs)
+    return (x if h is None else h), z
 
-    def call(st):
-        h = h_out if h_out is not None else (
-            None if y is None else torch.empty((B, N, C), dtype=x.dtype, device=x.device))
-        z = zs = None
-        z_b = z_n = 0
-        if want_z and quantize:
-            z = torch.empty((B * N, -(-C // 16) * 16), dtype=torch.int8, device=x.device)
-            zs = torch.empty(B * N, dtype=torch.float32, device=x.device)
-            z_n = z.stride(0)
-            z_b = N * z_n
-        elif want_z:
-            z = torch.empty((B, N, C), dtype=z_dtype, device=x.device)
-            z_b, z_n = N * C, C
-        h_b, h_n = (h.stride(0), h.stride(1)) if h is not None else (0, 0)
-        y_b, y_n = (y.stride(0), y.stride(1)) if y is not None else (0, 0)
-        p = bsa_gate_norm_params(B, N, C, NORMS[pre], NORMS[post], DTYPES[x.dtype],
-                                 DTYPES[y.dtype] if y is not None else 0, DTYPES[mod_dtype],
-                                 2 if quantize else DTYPES[z_dtype], eps, residual_scale,
-                                 branch_scale, x.stride(0), x.stride(1), y_b, y_n, h_b, h_n, z_b,
-                                 z_n, *gs, *ss, *hs)
-        i = bsa_gate_norm_inputs(*[_addr(t) for t in (x, y, gate, scale, shift, post_weight,
-                                                      post_bias, pre_weight, pre_bias)])
-        _check(lib().bsa_gate_norm(ctypes.byref(p), ctypes.byref(i), _addr(h), _addr(z), _addr(zs),
-                                   st), "bsa_gate_norm")
-        if want_z and quantize:
-            z = (z[:, :C], zs)
-        return (x if h is None else h), z
 
-    return _run(x, stream, where, call)
+@functools.lru_cache(maxsize=256)
+def _quantize_int8_plan(x):
+    where = "quantize_int8"
+    device = _one_device(where, x)
+    dtype, shape, st, _ = x
+    _need(dtype in _FLOATS and 2 <= len(shape) <= 4 and (shape[-1] == 1 or st[-1] == 1), where)
+    if len(shape) == 4:
+        (B, S, N, L), s = shape, (st[0], st[2], st[1])
+    elif len(shape) == 3:
+        (B, N, L), S, s = shape, 1, (st[0], st[1], 0)
+    else:
+        B, (N, L), S, s = 1, shape, 1, (0, st[0], 0)
+    K = S * L
+    ld = -(-K // 16) * 16
+    p = bsa_quantize_int8_params(B, N, S, L, DTYPES[dtype], *s, ld)
+    return device, ctypes.byref(p), B * N, K, ld
 
 
 def quantize_int8(x, stream=None):
     """bsa_quantize_int8: (codes, scales) of the rows of x [M, K] or [B, N, K], or of the token rows
     of an attention output [B, H, N, D] (H D values a token).  codes int8 [rows, K] (row stride a
     multiple of 16), scales fp32 [rows]."""
-    where = "quantize_int8"
-    _same_device(where, x)
-    _need(x.dtype in (torch.bfloat16, torch.float32) and 2 <= x.dim() <= 4 and x.stride(-1) == 1,
-          where)
-    if x.dim() == 4:
-        (B, S, N, L), s = x.shape, (x.stride(0), x.stride(2), x.stride(1))
-    elif x.dim() == 3:
-        (B, N, L), S, s = x.shape, 1, (x.stride(0), x.stride(1), 0)
-    else:
-        B, (N, L), S, s = 1, x.shape, 1, (0, x.stride(0), 0)
-    K = S * L
+    device, p, rows, K, ld = _quantize_int8_plan(_sig(x))
+    if not _here(device, stream):
+        with _elsewhere(device, stream, "quantize_int8"):
+            return quantize_int8(x)
+    codes = torch.empty((rows, ld), dtype=torch.int8, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _check(lib().bsa_quantize_int8(p, x.data_ptr(), codes.data_ptr(), scale.data_ptr(),
+                                   _raw_stream(device)), "bsa_quantize_int8")
+    return (codes if ld == K else codes[:, :K]), scale
 
-    def call(st):
-        codes = torch.empty((B * N, -(-K // 16) * 16), dtype=torch.int8, device=x.device)
-        scale = torch.empty(B * N, dtype=torch.float32, device=x.device)
-        p = bsa_quantize_int8_params(B, N, S, L, DTYPES[x.dtype], *s, codes.stride(0))
-        _check(lib().bsa_quantize_int8(ctypes.byref(p), _addr(x), _addr(codes), _addr(scale), st),
-               "bsa_quantize_int8")
-        return codes[:, :K], scale
 
-    return _run(x, stream, where, call)
+@functools.lru_cache(maxsize=256)
+def _linear_int8_plan(a, a_scale, w, w_scale, bias, out, out_dtype):
+    where = "linear_int8"
+    device = _one_device(where, a, a_scale, w, w_scale, bias, out)
+    for g in (a, w):
+        _need(g[0] is torch.int8 and len(g[1]) == 2 and (g[1][1] == 1 or g[2][1] == 1), where)
+    _need(a[1][1] == w[1][1] and a_scale is not None and w_scale is not None, where)
+    (M, K), N = a[1], w[1][0]
+    _vector(a_scale, M, where)
+    _vector(w_scale, N, where)
+    _vector(bias, N, where)
+    if out is not None:
+        out_dtype = out[0]
+        _need(out[1] == (M, N) and (N == 1 or out[2][1] == 1), where)
+    _need(out_dtype in _FLOATS, where)
+    return device, (M, N, K, DTYPES[out_dtype], a[2][0], w[2][0], N if out is None else out[2][0])
 
 
 def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=None,
                 dev_status=None, stream=None):
     """bsa_linear_int8: a_scale[:, None] * w_scale * (a @ w.T) + bias from int8 codes a [M, K] and
     w [N, K] (rows on 16 bytes, as ``quantize_int8`` lays them out), exact sums, fp32 or bf16 out."""
-    where = "linear_int8"
-    _same_device(where, a, a_scale, w, w_scale, bias, out, dev_status)
-    _need(a.dim() == 2 and w.dim() == 2 and a.dtype == w.dtype == torch.int8
-          and a.stride(1) == w.stride(1) == 1 and a.shape[1] == w.shape[1], where)
-    (M, K), N = a.shape, w.shape[0]
-    for t, n in ((a_scale, M), (w_scale, N)):
-        _need(t is not None, where)
-        _vector(t, n, where)
-    _vector(bias, N, where)
-    _need(out is None or (out.shape == (M, N) and out.stride(1) == 1
-                          and out.dtype in (torch.bfloat16, torch.float32)), where)
-
-    def call(st):
-        o = out if out is not None else torch.empty((M, N), dtype=out_dtype, device=a.device)
-        p = bsa_linear_int8_params(M, N, K, DTYPES[o.dtype], a.stride(0), w.stride(0), o.stride(0),
-                                   _addr(dev_status))
-        _check(lib().bsa_linear_int8(ctypes.byref(p), _addr(a), _addr(a_scale), _addr(w),
-                                     _addr(w_scale), _addr(bias), _addr(o), st), "bsa_linear_int8")
-        return o
-
-    return _run(a, stream, where, call)
+    device, p = _linear_int8_plan(_sig(a), _sig(a_scale), _sig(w), _sig(w_scale), _sig(bias),
+                                  _sig(out), out_dtype)
+    if not _here(device, stream):
+        with _elsewhere(device, stream, "linear_int8"):
+            return linear_int8(a, a_scale, w, w_scale, bias, out_dtype, out, dev_status)
+    o = out if out is not None else torch.empty(p[:2], dtype=out_dtype, device=a.device)
+    _check(lib().bsa_linear_int8(ctypes.byref(bsa_linear_int8_params(*p, _addr(dev_status))),
+                                 a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+                                 _addr(bias), o.data_ptr(), _raw_stream(device)), "bsa_linear_int8")
+    return o
 
 
 # --------------------------------------------------------------- allocation helpers

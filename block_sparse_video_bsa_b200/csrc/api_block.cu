@@ -240,6 +240,7 @@ int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs
   a.B = p->B, a.N = p->N, a.C = p->C, a.pre = p->pre, a.post = p->post;
   a.y_fp32 = p->y_dtype == BSA_DTYPE_FP32, a.mod_fp32 = p->mod_dtype == BSA_DTYPE_FP32;
   a.z_type = p->z_dtype;
+  a.dev_status = p->dev_status;
   a.eps = p->eps, a.residual_scale = p->residual_scale, a.branch_scale = p->branch_scale;
   a.x_b = p->x_b, a.x_n = p->x_n, a.y_b = p->y_b, a.y_n = p->y_n, a.h_b = p->h_b, a.h_n = p->h_n;
   a.z_b = p->z_b, a.z_n = p->z_n, a.gate_b = p->gate_b, a.gate_n = p->gate_n;

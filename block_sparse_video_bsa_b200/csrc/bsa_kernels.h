@@ -205,6 +205,7 @@ struct GateNormArgs {
   float eps, residual_scale, branch_scale;
   int64_t x_b, x_n, y_b, y_n, h_b, h_n, z_b, z_n;
   int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;
+  int* dev_status;
 };
 cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, bool vec, cudaStream_t st);
 

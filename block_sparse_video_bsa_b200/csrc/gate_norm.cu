@@ -7,9 +7,17 @@
 // as bf16 or fp32, or as int8 codes with one scale a row for the projection
 // that follows.
 //
-// HBM-bound: x and y are read once and h and z written once; a row stays in
-// registers between its sums.  All sums and statistics are fp32, z is formed
-// from the unrounded h.  The vectors that rows share come from L1 / L2.
+// HBM-bound: x and y are read once and h and z written once.  All sums and
+// statistics are fp32, z is formed from the unrounded h.
+//
+// Two kernels.  gate_norm_ring_kernel for many aligned rows whose vectors are
+// shared by the tokens: one CTA per SM keeps the vectors folded together in
+// shared memory (three or four loads a row saved), a producer warp streams
+// rows through a ring of shared-memory stages with bulk copies, and several
+// groups of warps each take the next row, so that the loads in flight do not
+// depend on registers and one group's reductions hide behind another's work.
+// gate_norm_kernel for the rest: one CTA a row, the row in registers between
+// its sums, the vectors from L1 / L2.
 #include "bsa_kernels.h"
 #include "rows.cuh"
 
@@ -17,13 +25,14 @@ namespace bsa {
 
 namespace {
 
+// ------------------------------------------------------------ one CTA a row
+
 // v = norm(v) * weight + bias, in registers
 template <int CH, bool kVec>
-__device__ __forceinline__ void norm_row(float (&v)[CH][8], int n, int kind, float eps,
-                                         const float* weight, const float* bias, RowReduce& red,
-                                         int& turn) {
+__device__ __forceinline__ void norm_row(RowGroup& g, float (&v)[CH][8], int n, int kind, float eps,
+                                         const float* weight, const float* bias) {
   if (kind == kNormLayer) {
-    const float2 mv = row_moments<CH, kVec>(v, n, red, turn);
+    const float2 mv = row_moments<CH, kVec>(g, v, n);
     const float rs = rsqrtf(mv.y + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -35,7 +44,7 @@ __device__ __forceinline__ void norm_row(float (&v)[CH][8], int n, int kind, flo
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) q = fmaf(v[c][j], v[c][j], q);   // 0 past n
-    const float rs = rsqrtf(row_sum(q, red, turn) / n + eps);
+    const float rs = rsqrtf(row_sum(g, q) / n + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -45,7 +54,7 @@ __device__ __forceinline__ void norm_row(float (&v)[CH][8], int n, int kind, flo
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float w[8];
-      load_shared8<kVec>(weight, n, c, w);
+      load_shared8<kVec>(g, weight, n, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] *= w[j];
     }
@@ -54,7 +63,7 @@ __device__ __forceinline__ void norm_row(float (&v)[CH][8], int n, int kind, flo
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float w[8];
-      load_shared8<kVec>(bias, n, c, w);
+      load_shared8<kVec>(g, bias, n, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] += w[j];
     }
@@ -62,79 +71,368 @@ __device__ __forceinline__ void norm_row(float (&v)[CH][8], int n, int kind, flo
 }
 
 template <bool kVec>
-__device__ __forceinline__ void load_mod8(const void* p, int fp32, int64_t off, int n, int c,
-                                          float v[8]) {
+__device__ __forceinline__ void load_mod8(const RowGroup& g, const void* p, int fp32, int64_t off,
+                                          int n, int c, float v[8]) {
   if (fp32)
-    load_shared8<kVec>(static_cast<const float*>(p) + off, n, c, v);
+    load_shared8<kVec>(g, static_cast<const float*>(p) + off, n, c, v);
   else
-    load_shared8<kVec>(static_cast<const __nv_bfloat16*>(p) + off, n, c, v);
+    load_shared8<kVec>(g, static_cast<const __nv_bfloat16*>(p) + off, n, c, v);
 }
 
-template <class Tx, int CH, int kThreads, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) gate_norm_kernel(const GateNormArgs a) {
+template <bool kVec>
+__device__ __forceinline__ void store_z8(const RowGroup& g, const GateNormArgs& a, int64_t o, int c,
+                                         const float v[8]) {
+  if (a.z_type == kTypeBf16)
+    store8<kVec>(g, static_cast<__nv_bfloat16*>(a.z) + o, a.C, c, v);
+  else if (a.z_type == kTypeFp32)
+    store8<kVec>(g, static_cast<float*>(a.z) + o, a.C, c, v);
+}
+
+template <class Tx, int CH, int kThreads, int kBlocks, bool kVec>
+__global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const GateNormArgs a) {
   __shared__ RowReduce red;
-  int turn = 0;
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int64_t b = row / a.N, t = row - b * a.N;
     float h[CH][8];
-    load_row<CH, kVec>(static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, a.C, h);
+    load_row<CH, kVec>(g, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, a.C, h);
     if (a.y) {
       float y[CH][8];
+      const int64_t o = b * a.y_b + t * a.y_n;
       if (a.y_fp32)
-        load_row<CH, kVec>(static_cast<const float*>(a.y) + b * a.y_b + t * a.y_n, a.C, y);
+        load_row<CH, kVec>(g, static_cast<const float*>(a.y) + o, a.C, y);
       else
-        load_row<CH, kVec>(static_cast<const __nv_bfloat16*>(a.y) + b * a.y_b + t * a.y_n, a.C, y);
-      norm_row<CH, kVec>(y, a.C, a.post, a.eps, a.post_weight, a.post_bias, red, turn);
+        load_row<CH, kVec>(g, static_cast<const __nv_bfloat16*>(a.y) + o, a.C, y);
+      norm_row<CH, kVec>(g, y, a.C, a.post, a.eps, a.post_weight, a.post_bias);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (a.gate) {
-          float g[8];
-          load_mod8<kVec>(a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.C, c, g);
+          float m[8];
+          load_mod8<kVec>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.C, c, m);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[c][j] *= g[j];
+          for (int j = 0; j < 8; ++j) y[c][j] *= m[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           h[c][j] = fmaf(y[c][j], a.branch_scale, h[c][j] * a.residual_scale);
-          if (row_index<kVec>(c, j) >= a.C) h[c][j] = 0.f;   // a bias reached past the row
+          if (row_index<kVec>(g, c, j) >= a.C) h[c][j] = 0.f;   // a norm reached past the row
         }
-        if (a.h) store8<kVec>(static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n, a.C, c, h[c]);
+        if (a.h) store8<kVec>(g, static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n, a.C, c, h[c]);
       }
     }
     if (!a.z) continue;
-    norm_row<CH, kVec>(h, a.C, a.pre, a.eps, a.pre_weight, a.pre_bias, red, turn);
+    norm_row<CH, kVec>(g, h, a.C, a.pre, a.eps, a.pre_weight, a.pre_bias);
+    const int64_t o = b * a.z_b + t * a.z_n;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (a.mscale) {
-        float g[8];
-        load_mod8<kVec>(a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.C, c, g);
+        float m[8];
+        load_mod8<kVec>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.C, c, m);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], g[j], h[c][j]);
+        for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], m[j], h[c][j]);
       }
       if (a.shift) {
-        float g[8];
-        load_mod8<kVec>(a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.C, c, g);
+        float m[8];
+        load_mod8<kVec>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.C, c, m);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] += g[j];
+        for (int j = 0; j < 8; ++j) h[c][j] += m[j];
       }
-      const int64_t o = b * a.z_b + t * a.z_n;
-      if (a.z_type == kTypeBf16)
-        store8<kVec>(static_cast<__nv_bfloat16*>(a.z) + o, a.C, c, h[c]);
-      else if (a.z_type == kTypeFp32)
-        store8<kVec>(static_cast<float*>(a.z) + o, a.C, c, h[c]);
+      store_z8<kVec>(g, a, o, c, h[c]);
     }
     if (a.z_type == kTypeInt8) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (row_index<kVec>(c, j) >= a.C) h[c][j] = 0.f;   // a layer norm's mean reached past the row
-      const float s = store_codes<CH, kVec>(h, a.C, static_cast<int8_t*>(a.z) + b * a.z_b + t * a.z_n,
-                                            red, turn);
-      if (threadIdx.x == 0) a.z_scale[row] = s;
+          if (row_index<kVec>(g, c, j) >= a.C) h[c][j] = 0.f;   // a layer norm's mean reached past the row
+      const float s = store_codes<CH, kVec>(g, h, a.C, static_cast<int8_t*>(a.z) + o);
+      if (g.tid == 0) a.z_scale[row] = s;
     }
   }
+}
+
+// ------------------------------------------------------------ rows through a ring
+
+constexpr int kRingThreads = 704;      // 21 warps of rows at most, and the producer warp
+constexpr int kMaxGroups = 15;         // named barriers
+constexpr int kMaxStages = 16;
+constexpr uint32_t kRingSmem = 227 * 1024;
+
+struct RingCtl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  int abort_flag;
+};
+
+// What shared memory holds, in floats and bytes.
+struct RingShape {
+  int threads, groups, stages;   // threads of a group
+  int has_gain, has_post_bias;   // gate * post_weight, gate * post_bias
+  int has_a, has_b;              // pre_weight (1 + scale), pre_bias (1 + scale) + shift
+  uint32_t x_bytes, y_bytes;     // of a row
+  uint32_t off_stage, off_red, off_ctl, bytes;
+};
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Chunk c of a row in shared memory (the chunk lies inside the row).
+__device__ __forceinline__ void smem8(const __nv_bfloat16* p, int i, float v[8]) {
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p + i), v);
+}
+__device__ __forceinline__ void smem8(const float* p, int i, float v[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p + i);
+  const float4 b = *reinterpret_cast<const float4*>(p + i + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// Mean and reciprocal root of a row that `get` reads chunk by chunk.
+template <int CH, class Get>
+__device__ __forceinline__ float2 row_stat(RowGroup& g, int n, int kind, float eps, Get get) {
+  if (kind == kNormNone) return make_float2(0.f, 1.f);
+  if (kind == kNormRms) {
+    float q = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = row_index<true>(g, c, 0);
+      if (i < n) {
+        float v[8];
+        get(c, i, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q = fmaf(v[j], v[j], q);
+      }
+    }
+    return make_float2(0.f, rsqrtf(row_sum(g, q) / n + eps));
+  }
+  // as row_moments (rows.cuh), over chunks that are read again
+  float s = 0.f, cnt = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = row_index<true>(g, c, 0);
+    if (i < n) {
+      float v[8];
+      get(c, i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+      cnt += 8.f;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+  }
+  const float mean = cnt > 0.f ? s / cnt : 0.f;
+  float q = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = row_index<true>(g, c, 0);
+    if (i < n) {
+      float v[8];
+      get(c, i, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q = fmaf(v[j] - mean, v[j] - mean, q);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+  const float2 mv = combine_moments(g, mean, q, cnt, n);
+  return make_float2(mv.x, rsqrtf(mv.y + eps));
+}
+
+template <class Tx, class Ty, int CH>
+__global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const GateNormArgs a,
+                                                                        const RingShape s) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  RingCtl* ctl = reinterpret_cast<RingCtl*>(sm + s.off_ctl);
+  const int rows_threads = s.groups * s.threads;
+  const int64_t b = blockIdx.y;
+  const int C = a.C;
+  float* gain = reinterpret_cast<float*>(sm);                    // branch_scale gate post_weight
+  float* pbias = gain + (s.has_gain ? C : 0);                    // branch_scale gate post_bias
+  float* va = pbias + (s.has_post_bias ? C : 0);                 // pre_weight (1 + scale)
+  float* vb = va + (s.has_a ? C : 0);                            // pre_bias (1 + scale) + shift
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < s.stages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], s.threads);
+    }
+    ctl->abort_flag = 0;
+    fence_barrier_init();
+  }
+  auto mod = [&](const void* p, int64_t off, int i) {
+    return a.mod_fp32 ? __ldg(static_cast<const float*>(p) + off + i)
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[off + i]);
+  };
+  for (int i = threadIdx.x; i < C; i += blockDim.x) {
+    const float gt = a.gate ? mod(a.gate, b * a.gate_b, i) : 1.f;
+    const float sc = a.mscale ? 1.f + mod(a.mscale, b * a.scale_b, i) : 1.f;
+    const float sh = a.shift ? mod(a.shift, b * a.shift_b, i) : 0.f;
+    if (s.has_gain) gain[i] = a.branch_scale * gt * (a.post_weight ? __ldg(a.post_weight + i) : 1.f);
+    if (s.has_post_bias) pbias[i] = a.branch_scale * gt * __ldg(a.post_bias + i);
+    if (s.has_a) va[i] = sc * (a.pre_weight ? __ldg(a.pre_weight + i) : 1.f);
+    if (s.has_b) vb[i] = fmaf(a.pre_bias ? __ldg(a.pre_bias + i) : 0.f, sc, sh);
+  }
+  __syncthreads();
+  const WaitCtx wc{&ctl->abort_flag, a.dev_status};
+  const uint32_t stage_bytes = s.x_bytes + s.y_bytes;
+  const int64_t step = gridDim.x;
+
+  if (static_cast<int>(threadIdx.x) >= rows_threads) {
+    if (static_cast<int>(threadIdx.x) == rows_threads) {
+      int64_t i = 0;
+      for (int64_t t = blockIdx.x; t < a.N; t += step, ++i) {
+        const int st = static_cast<int>(i % s.stages);
+        if (i >= s.stages && !mbar_wait(&ctl->empty[st], ((i / s.stages) - 1) & 1, wc)) break;
+        uint8_t* dst = sm + s.off_stage + st * stage_bytes;
+        mbar_arrive_expect_tx(&ctl->full[st], stage_bytes);
+        bulk_load(dst, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, s.x_bytes,
+                  &ctl->full[st]);
+        if (s.y_bytes)
+          bulk_load(dst + s.x_bytes, static_cast<const Ty*>(a.y) + b * a.y_b + t * a.y_n, s.y_bytes,
+                    &ctl->full[st]);
+      }
+      // every issued load has landed before the CTA exits
+      for (int64_t k = (i > s.stages ? i - s.stages : 0); k < i; ++k)
+        mbar_wait(&ctl->full[k % s.stages], (k / s.stages) & 1, wc);
+    }
+    return;
+  }
+
+  const int group = threadIdx.x / s.threads;
+  RowGroup g{static_cast<int>(threadIdx.x) - group * s.threads, s.threads, 1 + group,
+             reinterpret_cast<RowReduce*>(sm + s.off_red) + group, 0};
+  for (int64_t i = group;; i += s.groups) {
+    const int64_t t = blockIdx.x + i * step;
+    if (t >= a.N) break;
+    const int st = static_cast<int>(i % s.stages);
+    // the whole group goes on or none of it
+    if (!g.all(mbar_wait(&ctl->full[st], (i / s.stages) & 1, wc))) break;
+    const Tx* xs = reinterpret_cast<const Tx*>(sm + s.off_stage + st * stage_bytes);
+    const Ty* ys = reinterpret_cast<const Ty*>(sm + s.off_stage + st * stage_bytes + s.x_bytes);
+    float h[CH][8];
+    if (s.y_bytes) {
+      const float2 mr = row_stat<CH>(g, C, a.post, a.eps, [&](int, int k, float v[8]) { smem8(ys, k, v); });
+      Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k = row_index<true>(g, c, 0);
+        if (k < C) {
+          float v[8], m[8];
+          smem8(ys, k, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = (v[j] - mr.x) * mr.y;
+          if (s.has_gain) {
+            smem8(gain, k, m);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= m[j];
+          }
+          if (s.has_post_bias) {
+            smem8(pbias, k, m);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += m[j];
+          }
+          smem8(xs, k, h[c]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], a.residual_scale, v[j]);
+          if (a.h) store8<true>(g, ho, C, c, h[c]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int k = row_index<true>(g, c, 0);
+        if (k < C) smem8(xs, k, h[c]);
+      }
+    }
+    mbar_arrive(&ctl->empty[st]);
+    if (!a.z) continue;
+    const float2 mr = row_stat<CH>(g, C, a.pre, a.eps, [&](int c, int, float v[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = h[c][j];
+    });
+    const int64_t o = b * a.z_b + t * a.z_n;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = row_index<true>(g, c, 0);
+      if (k < C) {
+        float m[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] = (h[c][j] - mr.x) * mr.y;
+        if (s.has_a) {
+          smem8(va, k, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[c][j] *= m[j];
+        }
+        if (s.has_b) {
+          smem8(vb, k, m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[c][j] += m[j];
+        }
+        store_z8<true>(g, a, o, c, h[c]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] = 0.f;
+      }
+    }
+    if (a.z_type == kTypeInt8) {
+      const float sc = store_codes<CH, true>(g, h, C, static_cast<int8_t*>(a.z) + o);
+      if (g.tid == 0) a.z_scale[b * a.N + t] = sc;
+    }
+  }
+}
+
+// The ring's shape for these rows, or false where the other kernel runs: rows
+// that are short (their loads are in flight enough with one CTA a row), few,
+// or too long for two of them beside the vectors in shared memory.
+bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3* grid) {
+  const bool token = (a.gate && a.gate_n) || (a.mscale && a.scale_n) || (a.shift && a.shift_n);
+  if (token) return false;
+  const int per = 148 / a.B > 0 ? 148 / a.B : 1;
+  if (a.N < 4 * per || a.B > 65535) return false;
+  s->x_bytes = static_cast<uint32_t>(a.C) * (x_fp32 ? 4 : 2);
+  s->y_bytes = a.y ? static_cast<uint32_t>(a.C) * (a.y_fp32 ? 4 : 2) : 0;
+  if (s->x_bytes + s->y_bytes < 4096) return false;
+  const int vecs = a.C / 8;
+  *ch = 4;
+  s->threads = ((vecs + 3) / 4 + 31) / 32 * 32;
+  if (s->threads > kRingThreads - 32) return false;
+  s->groups = (kRingThreads - 32) / s->threads;
+  if (s->groups > kMaxGroups) s->groups = kMaxGroups;
+  s->has_gain = a.y && (a.gate || a.post_weight || a.branch_scale != 1.f);
+  s->has_post_bias = a.y && a.post_bias;
+  s->has_a = a.z && (a.mscale || a.pre_weight);
+  s->has_b = a.z && (a.shift || a.pre_bias);
+  const uint32_t vectors = (s->has_gain + s->has_post_bias + s->has_a + s->has_b) * a.C * 4u;
+  s->off_stage = (vectors + 127) & ~127u;
+  const uint32_t fixed = s->groups * static_cast<uint32_t>(sizeof(RowReduce)) + sizeof(RingCtl) + 16;
+  const uint32_t stage = s->x_bytes + s->y_bytes;
+  if (s->off_stage + fixed + 2 * stage > kRingSmem) return false;
+  int stages = static_cast<int>((kRingSmem - s->off_stage - fixed) / stage);
+  s->stages = stages < kMaxStages ? stages : kMaxStages;
+  s->off_red = (s->off_stage + s->stages * stage + 15) & ~15u;
+  s->off_ctl = s->off_red + s->groups * static_cast<uint32_t>(sizeof(RowReduce));
+  s->bytes = s->off_ctl + sizeof(RingCtl);
+  *grid = dim3(per, a.B);
+  return true;
+}
+
+template <class Tx, class Ty>
+cudaError_t launch_ring(const GateNormArgs& a, const RingShape& s, dim3 grid, cudaStream_t st) {
+  auto* kernel = gate_norm_ring_kernel<Tx, Ty, 4>;
+  static std::atomic<bool> done[64];
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  });
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, s.groups * s.threads + 32, s.bytes, st>>>(a, s);
+  return cudaGetLastError();
 }
 
 template <class Tx, bool kVec>
@@ -143,20 +441,20 @@ cudaError_t launch(const GateNormArgs& a, int ch, int threads, int blocks, cudaS
     k<<<blocks, threads, 0, st>>>(a);
     return cudaGetLastError();
   };
-  if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, kVec>);
-  if (ch == 2) return go(gate_norm_kernel<Tx, 2, 1024, kVec>);
-  if (threads <= 256) return go(gate_norm_kernel<Tx, 4, 256, kVec>);
-  if (threads <= 512) return go(gate_norm_kernel<Tx, 4, 512, kVec>);
-  return go(gate_norm_kernel<Tx, 4, 1024, kVec>);
+  if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, 1, kVec>);
+  if (ch == 2) return threads <= 512 ? go(gate_norm_kernel<Tx, 2, 512, 2, kVec>)
+                                     : go(gate_norm_kernel<Tx, 2, 1024, 1, kVec>);
+  return threads <= 512 ? go(gate_norm_kernel<Tx, 4, 512, 1, kVec>)
+                        : go(gate_norm_kernel<Tx, 4, 1024, 1, kVec>);
 }
 
 }  // namespace
 
-// Threads and chunks (1, 2 or 4) of a row of n <= 32,768 values: four chunks a
-// thread, fewer for short rows and for few rows, where a row's latency counts.
+// Threads and chunks (1, 2 or 4) of a row of n <= 32,768 values: two chunks a
+// thread, one for short rows and for few rows, where a row's latency counts.
 void row_shape(int n, int64_t rows, int* ch, int* threads) {
   const int vecs = (n + 7) / 8;
-  int c = rows >= 148 * 2 ? 4 : 1;
+  int c = rows >= 148 * 2 ? 2 : 1;
   while (c > 1 && (vecs + c - 1) / c < 32) c /= 2;
   while ((vecs + c - 1) / c > 1024) c *= 2;
   *ch = c;
@@ -164,15 +462,25 @@ void row_shape(int n, int64_t rows, int* ch, int* threads) {
 }
 
 cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, bool vec, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.B) * a.N;
+  RingShape s = {};
   int ch, threads;
+  dim3 grid;
+  using bf16 = __nv_bfloat16;
+  if (vec && ring_shape(a, x_fp32, &s, &ch, &grid)) {
+    if (x_fp32)
+      return a.y_fp32 ? launch_ring<float, float>(a, s, grid, st)
+                      : launch_ring<float, bf16>(a, s, grid, st);
+    return a.y_fp32 ? launch_ring<bf16, float>(a, s, grid, st)
+                    : launch_ring<bf16, bf16>(a, s, grid, st);
+  }
+  const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   row_shape(a.C, rows, &ch, &threads);
   const int blocks = static_cast<int>(rows < (1 << 30) ? rows : (1 << 30));
   if (vec)
     return x_fp32 ? launch<float, true>(a, ch, threads, blocks, st)
-                  : launch<__nv_bfloat16, true>(a, ch, threads, blocks, st);
+                  : launch<bf16, true>(a, ch, threads, blocks, st);
   return x_fp32 ? launch<float, false>(a, ch, threads, blocks, st)
-                : launch<__nv_bfloat16, false>(a, ch, threads, blocks, st);
+                : launch<bf16, false>(a, ch, threads, blocks, st);
 }
 
 }  // namespace bsa

@@ -13,9 +13,9 @@ namespace bsa {
 namespace {
 
 template <class Tx, int CH, int kThreads, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1) quant_int8_kernel(const QuantInt8Args a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) quant_int8_kernel(const QuantInt8Args a) {
   __shared__ RowReduce red;
-  int turn = 0;
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   const int n = a.S * a.L;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -23,14 +23,14 @@ __global__ void __launch_bounds__(kThreads, 1) quant_int8_kernel(const QuantInt8
     const Tx* src = static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n;
     float x[CH][8];
     if (a.S == 1) {
-      load_row<CH, kVec>(src, n, x);
+      load_row<CH, kVec>(g, src, n, x);
     } else {
       if constexpr (kVec) {       // L is a multiple of 8: a chunk lies in one segment
         constexpr int W = static_cast<int>(sizeof(Tx)) / 2;   // 16-byte words a chunk
         uint4 w[CH][W];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-          const int i = row_index<true>(c, 0);
+          const int i = row_index<true>(g, c, 0);
           const int s = i / a.L;
 #pragma unroll
           for (int k = 0; k < W; ++k) {
@@ -55,13 +55,13 @@ __global__ void __launch_bounds__(kThreads, 1) quant_int8_kernel(const QuantInt8
         for (int c = 0; c < CH; ++c)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const int i = row_index<false>(c, j);
+            const int i = row_index<false>(g, c, j);
             const int s = i / a.L;
             x[c][j] = i < n ? to_f32(src[s * a.x_s + (i - s * a.L)]) : 0.f;
           }
       }
     }
-    const float s = store_codes<CH, kVec>(x, n, static_cast<int8_t*>(a.q) + row * a.q_ld, red, turn);
+    const float s = store_codes<CH, kVec>(g, x, n, a.q + row * a.q_ld);
     if (threadIdx.x == 0) a.scale[row] = s;
   }
 }

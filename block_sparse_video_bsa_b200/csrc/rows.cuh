@@ -1,9 +1,9 @@
-// One row of up to 32,768 values spread over a CTA: loads, stores, the row's
+// One row of up to 32,768 values spread over a CTA or a group of its warps: loads, stores, the row's
 // sums and the int8 codes of a row (gate_norm.cu, quant_int8.cu).
 //
 // A thread holds CH chunks of 8 values in registers.  kVec: chunk c of thread
-// t is the 8 neighbours at (c * blockDim + t) * 8, read and written as 16-byte
-// words; else value j of chunk c sits at (c * 8 + j) * blockDim + t, so that
+// t is the 8 neighbours at (c * threads + t) * 8, read and written as 16-byte
+// words; else value j of chunk c sits at (c * 8 + j) * threads + t, so that
 // scalar accesses of rows that do not start on 16 bytes are still contiguous
 // across a warp.  Everything done to a row is per value or a sum over all of
 // it, so the arrangement does not matter to it.
@@ -18,9 +18,42 @@ namespace bsa {
 // normal range.
 constexpr float kInt8Floor = 0x1p-100f;
 
+// Per-warp partials of a reduction over the threads of a row.  Uses alternate
+// between two slots, so one barrier a reduction is enough: before a slot is
+// written again every thread has passed the barrier of the reduction between.
+struct RowReduce {
+  float4 part[2][32];
+};
+
+// The threads that share a row: a whole CTA, or one of several groups of
+// warps in it, each with its own named barrier and partials.
+struct RowGroup {
+  int tid, threads;    // this thread and the number of threads (whole warps)
+  int bar;             // named barrier of the group
+  RowReduce* red;
+  int turn;            // slot of the next reduction
+  __device__ __forceinline__ int warps() const { return threads >> 5; }
+  __device__ __forceinline__ void sync() const {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+  }
+  // True on every thread when it is true on all (one barrier).
+  __device__ __forceinline__ bool all(bool ok) const {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %3, 0;\n\t"
+        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(bar), "r"(threads), "r"(static_cast<uint32_t>(ok))
+        : "memory");
+    return r != 0;
+  }
+};
+
 template <bool kVec>
-__device__ __forceinline__ int row_index(int c, int j) {
-  return kVec ? (c * blockDim.x + threadIdx.x) * 8 + j : (c * 8 + j) * blockDim.x + threadIdx.x;
+__device__ __forceinline__ int row_index(const RowGroup& g, int c, int j) {
+  return kVec ? (c * g.threads + g.tid) * 8 + j : (c * 8 + j) * g.threads + g.tid;
 }
 
 __device__ __forceinline__ uint4 ld_row_v4(const void* p) {
@@ -36,12 +69,12 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 
 // x[c][j] = p[...] (0 past n).  A row is read once: it skips L1.
 template <int CH, bool kVec>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int n, float (&x)[CH][8]) {
+__device__ __forceinline__ void load_row(const RowGroup& g, const __nv_bfloat16* p, int n, float (&x)[CH][8]) {
   if constexpr (kVec) {
     uint4 w[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = row_index<true>(c, 0);
+      const int i = row_index<true>(g, c, 0);
       w[c] = make_uint4(0, 0, 0, 0);
       if (i < n) w[c] = ld_row_v4(p + i);
     }
@@ -52,17 +85,17 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, int n, float (&
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(c, j);
+        const int i = row_index<false>(g, c, j);
         x[c][j] = i < n ? to_f32(p[i]) : 0.f;
       }
   }
 }
 template <int CH, bool kVec>
-__device__ __forceinline__ void load_row(const float* p, int n, float (&x)[CH][8]) {
+__device__ __forceinline__ void load_row(const RowGroup& g, const float* p, int n, float (&x)[CH][8]) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     if constexpr (kVec) {
-      const int i = row_index<true>(c, 0);
+      const int i = row_index<true>(g, c, 0);
       uint4 a = make_uint4(0, 0, 0, 0), b = a;
       if (i < n) a = ld_row_v4(p + i), b = ld_row_v4(p + i + 4);
       x[c][0] = __uint_as_float(a.x), x[c][1] = __uint_as_float(a.y);
@@ -72,7 +105,7 @@ __device__ __forceinline__ void load_row(const float* p, int n, float (&x)[CH][8
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(c, j);
+        const int i = row_index<false>(g, c, j);
         x[c][j] = i < n ? p[i] : 0.f;
       }
     }
@@ -81,9 +114,9 @@ __device__ __forceinline__ void load_row(const float* p, int n, float (&x)[CH][8
 
 // One chunk of a vector that many rows share (kept in L1).
 template <bool kVec>
-__device__ __forceinline__ void load_shared8(const float* p, int n, int c, float v[8]) {
+__device__ __forceinline__ void load_shared8(const RowGroup& g, const float* p, int n, int c, float v[8]) {
   if constexpr (kVec) {
-    const int i = row_index<true>(c, 0);
+    const int i = row_index<true>(g, c, 0);
     float4 a = make_float4(0, 0, 0, 0), b = a;
     if (i < n) {
       a = __ldg(reinterpret_cast<const float4*>(p + i));
@@ -93,22 +126,22 @@ __device__ __forceinline__ void load_shared8(const float* p, int n, int c, float
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(c, j);
+      const int i = row_index<false>(g, c, j);
       v[j] = i < n ? __ldg(p + i) : 0.f;
     }
   }
 }
 template <bool kVec>
-__device__ __forceinline__ void load_shared8(const __nv_bfloat16* p, int n, int c, float v[8]) {
+__device__ __forceinline__ void load_shared8(const RowGroup& g, const __nv_bfloat16* p, int n, int c, float v[8]) {
   if constexpr (kVec) {
-    const int i = row_index<true>(c, 0);
+    const int i = row_index<true>(g, c, 0);
     uint4 w = make_uint4(0, 0, 0, 0);
     if (i < n) w = __ldg(reinterpret_cast<const uint4*>(p + i));
     bf16x8_to_f32(w, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(c, j);
+      const int i = row_index<false>(g, c, j);
       v[j] = i < n ? __bfloat162float(p[i]) : 0.f;
     }
   }
@@ -116,24 +149,24 @@ __device__ __forceinline__ void load_shared8(const __nv_bfloat16* p, int n, int 
 
 // One chunk of a row, rounded once to the stored type (to nearest even).
 template <bool kVec>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, int c, const float v[8]) {
+__device__ __forceinline__ void store8(const RowGroup& g, __nv_bfloat16* p, int n, int c, const float v[8]) {
   if constexpr (kVec) {
-    const int i = row_index<true>(c, 0);
+    const int i = row_index<true>(g, c, 0);
     if (i < n)
       *reinterpret_cast<uint4*>(p + i) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                     pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(c, j);
+      const int i = row_index<false>(g, c, j);
       if (i < n) p[i] = __float2bfloat16_rn(v[j]);
     }
   }
 }
 template <bool kVec>
-__device__ __forceinline__ void store8(float* p, int n, int c, const float v[8]) {
+__device__ __forceinline__ void store8(const RowGroup& g, float* p, int n, int c, const float v[8]) {
   if constexpr (kVec) {
-    const int i = row_index<true>(c, 0);
+    const int i = row_index<true>(g, c, 0);
     if (i < n) {
       reinterpret_cast<float4*>(p + i)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(p + i)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -141,45 +174,61 @@ __device__ __forceinline__ void store8(float* p, int n, int c, const float v[8])
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(c, j);
+      const int i = row_index<false>(g, c, j);
       if (i < n) p[i] = v[j];
     }
   }
 }
 
-// Per-warp partials of a CTA-wide reduction.  Uses alternate between two
-// slots, so one barrier a reduction is enough: before a slot is written again
-// every thread has passed the barrier of the reduction between.
-struct RowReduce {
-  float4 part[2][32];
-};
-
-// Sum over the CTA; `turn` flips with every call.
-__device__ __forceinline__ float row_sum(float v, RowReduce& red, int& turn) {
+// Sum over the row's threads.
+__device__ __forceinline__ float row_sum(RowGroup& g, float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warps = blockDim.x >> 5;
+  const int warps = g.warps();
   if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) red.part[turn][threadIdx.x >> 5].x = v;
-  __syncthreads();
+  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5].x = v;
+  g.sync();
   v = 0.f;
-  for (int w = 0; w < warps; ++w) v += red.part[turn][w].x;
-  turn ^= 1;
+  for (int w = 0; w < warps; ++w) v += g.red->part[g.turn][w].x;
+  g.turn ^= 1;
   return v;
 }
 
-// Largest value over the CTA; v >= 0 or NaN, and a NaN anywhere wins (as an
+// Largest value over the row's threads; v >= 0 or NaN, and a NaN anywhere wins (as an
 // unsigned word it is above every number).
-__device__ __forceinline__ float row_max_abs(float v, RowReduce& red, int& turn) {
+__device__ __forceinline__ float row_max_abs(RowGroup& g, float v) {
   uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
-  const int warps = blockDim.x >> 5;
+  const int warps = g.warps();
   if (warps == 1) return __uint_as_float(m);
-  if ((threadIdx.x & 31) == 0) red.part[turn][threadIdx.x >> 5].x = __uint_as_float(m);
-  __syncthreads();
+  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5].x = __uint_as_float(m);
+  g.sync();
   m = 0;
-  for (int w = 0; w < warps; ++w) m = max(m, __float_as_uint(red.part[turn][w].x));
-  turn ^= 1;
+  for (int w = 0; w < warps; ++w) m = max(m, __float_as_uint(g.red->part[g.turn][w].x));
+  g.turn ^= 1;
   return __uint_as_float(m);
+}
+
+// Mean and mean squared deviation of a row of n values from each warp's own
+// mean, sum of squares about it and count (exact identity, one barrier).
+__device__ __forceinline__ float2 combine_moments(RowGroup& g, float mean, float q, float cnt,
+                                                  int n) {
+  const int warps = g.warps();
+  if (warps == 1) return make_float2(mean, q / n);
+  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5] = make_float4(mean, q, cnt, 0.f);
+  g.sync();
+  float total = 0.f;
+  for (int w = 0; w < warps; ++w) {
+    const float4 p = g.red->part[g.turn][w];
+    total = fmaf(p.x, p.z, total);
+  }
+  const float all = total / n;
+  float m2 = 0.f;
+  for (int w = 0; w < warps; ++w) {
+    const float4 p = g.red->part[g.turn][w];
+    m2 += fmaf((p.x - all) * (p.x - all), p.z, p.y);
+  }
+  g.turn ^= 1;
+  return make_float2(all, m2 / n);
 }
 
 // Mean and mean squared deviation of the row's n values.  Each warp takes the
@@ -187,18 +236,17 @@ __device__ __forceinline__ float row_max_abs(float v, RowReduce& red, int& turn)
 // combined exactly (sum of squares + counts x squared distance of the means):
 // no difference of large sums, and one barrier.
 template <int CH, bool kVec>
-__device__ __forceinline__ float2 row_moments(const float (&x)[CH][8], int n, RowReduce& red,
-                                              int& turn) {
+__device__ __forceinline__ float2 row_moments(RowGroup& g, const float (&x)[CH][8], int n) {
   float s = 0.f, cnt = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) s += x[c][j];          // 0 past n
     if constexpr (kVec) {
-      cnt += row_index<true>(c, 0) < n ? 8.f : 0.f;
+      cnt += row_index<true>(g, c, 0) < n ? 8.f : 0.f;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cnt += row_index<false>(c, j) < n ? 1.f : 0.f;
+      for (int j = 0; j < 8; ++j) cnt += row_index<false>(g, c, j) < n ? 1.f : 0.f;
     }
   }
 #pragma unroll
@@ -212,29 +260,13 @@ __device__ __forceinline__ float2 row_moments(const float (&x)[CH][8], int n, Ro
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const bool in = row_index<kVec>(c, j) < n;
+      const bool in = row_index<kVec>(g, c, j) < n;
       const float d = x[c][j] - mean;
       q = in ? fmaf(d, d, q) : q;
     }
 #pragma unroll
   for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return make_float2(mean, q / n);
-  if ((threadIdx.x & 31) == 0) red.part[turn][threadIdx.x >> 5] = make_float4(mean, q, cnt, 0.f);
-  __syncthreads();
-  float total = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    const float4 p = red.part[turn][w];
-    total = fmaf(p.x, p.z, total);
-  }
-  const float all = total / n;
-  float m2 = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    const float4 p = red.part[turn][w];
-    m2 += fmaf((p.x - all) * (p.x - all), p.z, p.y);
-  }
-  turn ^= 1;
-  return make_float2(all, m2 / n);
+  return combine_moments(g, mean, q, cnt, n);
 }
 
 // int8 codes of a row: scale = amax / 127, code = rint(x * (127 / amax)), both
@@ -242,8 +274,7 @@ __device__ __forceinline__ float2 row_moments(const float (&x)[CH][8], int n, Ro
 // infinity has a scale that is not finite (NaN) and codes 0: its products are
 // NaN.  Stores 8 (or single) codes; returns the scale to every thread.
 template <int CH, bool kVec>
-__device__ __forceinline__ float store_codes(const float (&x)[CH][8], int n, int8_t* q,
-                                             RowReduce& red, int& turn) {
+__device__ __forceinline__ float store_codes(RowGroup& g, const float (&x)[CH][8], int n, int8_t* q) {
   float m = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
@@ -252,7 +283,7 @@ __device__ __forceinline__ float store_codes(const float (&x)[CH][8], int n, int
       const uint32_t a = __float_as_uint(x[c][j]) & 0x7fffffffu;   // 0 past n
       m = __uint_as_float(max(__float_as_uint(m), a));
     }
-  m = row_max_abs(m, red, turn);
+  m = row_max_abs(g, m);
   const bool finite = m <= 3.402823466e38f;
   m = finite ? fmaxf(m, kInt8Floor) : m;
   const float inv = finite ? __fdiv_rn(127.f, m) : 0.f;
@@ -262,7 +293,7 @@ __device__ __forceinline__ float store_codes(const float (&x)[CH][8], int n, int
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = finite ? __float2int_rn(__fmul_rn(x[c][j], inv)) : 0;
     if constexpr (kVec) {
-      const int i = row_index<true>(c, 0);
+      const int i = row_index<true>(g, c, 0);
       if (i < n) {
         uint32_t lo = 0, hi = 0;
 #pragma unroll
@@ -275,7 +306,7 @@ __device__ __forceinline__ float store_codes(const float (&x)[CH][8], int n, int
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(c, j);
+        const int i = row_index<false>(g, c, j);
         if (i < n) q[i] = static_cast<int8_t>(v[j]);
       }
     }

@@ -588,6 +588,7 @@ typedef struct {
   float eps, residual_scale, branch_scale;
   int64_t x_b, x_n, y_b, y_n, h_b, h_n, z_b, z_n;
   int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;  /* 0: shared   */
+  int32_t* dev_status;           /* as bsa_params                             */
 } bsa_gate_norm_params;
 
 typedef struct {

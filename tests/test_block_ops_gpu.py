@@ -422,3 +422,58 @@ def test_calls_are_deterministic_and_captured(cuda_dev):
     for g, outs in graphs:
         for a, b in zip(first, outs):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ many rows (the streamed kernel)
+
+RING = [
+    # B, N, C, pre, post, x, y, mod shape, affine
+    (1, 700, 7168, "layer", "rms", torch.bfloat16, torch.bfloat16, "b", True),
+    (2, 400, 2056, "rms", "layer", torch.bfloat16, torch.float32, "b1", True),
+    (3, 333, 1032, "layer", "none", torch.float32, torch.bfloat16, "c", False),
+    (1, 601, 1024, "none", "rms", torch.float32, torch.float32, "c", False),
+    (150, 5, 2048, "rms", "rms", torch.bfloat16, torch.bfloat16, "b", True),
+    (1, 593, 12288, "layer", "none", torch.bfloat16, torch.bfloat16, "c", False),
+]
+
+
+@pytest.mark.parametrize("B,N,C,pre,post,tx,ty,shape,aff", RING)
+def test_gate_norm_of_many_rows(cuda_dev, B, N, C, pre, post, tx, ty, shape, aff):
+    x, y = rnd(90, B, N, C, dtype=tx) + 3, rnd(91, B, N, C, dtype=ty) - 2
+    s = dict(b=(B, C), b1=(B, 1, C), c=(C,))[shape]
+    gate, scale, shift = (rnd(92 + i, *s, dtype=torch.bfloat16, scale=0.5) for i in range(3))
+    args = (x, y, gate, scale, shift, pre, post)
+    h, z, ws = run_gate_norm(*args, aff, 1e-6, 0.5, 2.0)
+    hr, zr, eh, ez = gate_norm_bounds(*args, ws, 1e-6, 0.5, 2.0)
+    close(h, hr, eh)
+    close(z, zr, ez)
+    _, (codes, top), _ = run_gate_norm(*args, aff, 1e-6, 0.5, 2.0, quantize=True)
+    err = np.abs(host(codes).reshape(zr.shape) * host(top).reshape(B, N, 1) - zr)
+    assert (err <= 0.5 * host(top).reshape(B, N, 1) * (1 + 2.0 ** -16) + 2 * ez.max(-1, keepdims=True)).all()
+    x2 = x.clone()
+    h2, z2, _ = run_gate_norm(x2, *args[1:], aff, 1e-6, 0.5, 2.0, h_out=x2, z_dtype=torch.float32)
+    assert torch.equal(h2, h) and torch.equal(z2.bfloat16(), z)
+    # each part left out
+    _, z3, ws3 = run_gate_norm(x, None, None, scale, None, pre, "none", aff, 1e-6)
+    _, zr3, _, ez3 = gate_norm_bounds(x, None, None, scale, None, pre, "none", ws3, 1e-6, 1.0, 1.0)
+    close(z3, zr3, ez3)
+    h4, none, ws4 = run_gate_norm(x, y, None, None, None, pre, post, False, 1e-6, want_z=False)
+    hr4, _, eh4, _ = gate_norm_bounds(x, y, None, None, None, pre, post, ws4, 1e-6, 1.0, 1.0)
+    assert none is None
+    close(h4, hr4, eh4)
+
+
+def test_gate_norm_of_many_rows_in_wider_buffers(cuda_dev):
+    # rows of a wider buffer and a NaN row: neighbours of both are untouched
+    B, N, C = 2, 400, 2048
+    x, y = rnd(95, B, N, C + 64)[..., 32:32 + C], rnd(96, B, N, C)
+    y[1, 7, 5] = float("nan")
+    buf = torch.full((B, N, C + 16), 3.0, device="cuda")
+    h, z = bsa.gate_norm(x, y, pre="layer", post="rms", h_out=buf[..., 8:8 + C])
+    assert (buf[..., :8] == 3).all() and (buf[..., 8 + C:] == 3).all()
+    assert z[1, 7].isnan().all() and h[1, 7].isnan().all()
+    keep = torch.ones(B, N, dtype=torch.bool, device="cuda")
+    keep[1, 7] = False
+    hr, zr, eh, ez = gate_norm_bounds(x[keep][None], y[keep][None], None, None, None, "layer", "rms", [None] * 4, 1e-6, 1.0, 1.0)
+    close(h[keep][None], hr, eh)
+    close(z[keep][None], zr, ez)
