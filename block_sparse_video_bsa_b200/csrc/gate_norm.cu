@@ -182,46 +182,78 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// Chunk c of a row in shared memory (the chunk lies inside the row).
-__device__ __forceinline__ void smem8(const __nv_bfloat16* p, int i, float v[8]) {
-  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p + i), v);
+// 8 values as four pairs: the packed fp32 instructions halve the arithmetic,
+// which is what bounds this kernel next to HBM.
+struct Oct {
+  float2 p[4];
+};
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void smem8(const __nv_bfloat16* p, Oct& v) {
+  const uint4 w = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v.p[j] = make_float2(__uint_as_float(u[j] << 16), __uint_as_float(u[j] & 0xffff0000u));
 }
-__device__ __forceinline__ void smem8(const float* p, int i, float v[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p + i);
-  const float4 b = *reinterpret_cast<const float4*>(p + i + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void smem8(const float* p, Oct& v) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v.p[0] = make_float2(a.x, a.y), v.p[1] = make_float2(a.z, a.w);
+  v.p[2] = make_float2(b.x, b.y), v.p[3] = make_float2(b.z, b.w);
 }
 
-// Mean and reciprocal root of a row that `get` reads chunk by chunk.
+// A vector folded in shared memory: the 8 values of 32 neighbouring threads
+// are kept as their first fours, then their second fours, so that a warp's
+// 16-byte loads meet every bank once.  at: where value i lies; load: chunk k / 8.
+__device__ __forceinline__ int folded_at(int i) {
+  return (i & ~255) | ((i & 4) << 5) | ((i & 248) >> 1) | (i & 3);
+}
+__device__ __forceinline__ void folded8(const float* p, int k, Oct& v) {
+  const int at = folded_at(k);
+  const float4 a = *reinterpret_cast<const float4*>(p + at);
+  const float4 b = *reinterpret_cast<const float4*>(p + at + 128);
+  v.p[0] = make_float2(a.x, a.y), v.p[1] = make_float2(a.z, a.w);
+  v.p[2] = make_float2(b.x, b.y), v.p[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const Oct& v) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v.p[0].x, v.p[0].y), pack_bf16x2(v.p[1].x, v.p[1].y),
+                 pack_bf16x2(v.p[2].x, v.p[2].y), pack_bf16x2(v.p[3].x, v.p[3].y));
+}
+__device__ __forceinline__ void put8(float* p, const Oct& v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
+}
+
+// (m, r) with norm(v) = v r + m for a row that `get` gives chunk by chunk;
+// in[c]: the chunk lies inside the row (the others are copies of its last).
 template <int CH, class Get>
-__device__ __forceinline__ float2 row_stat(RowGroup& g, int n, int kind, float eps, Get get) {
+__device__ __forceinline__ float2 row_affine(RowGroup& g, int n, int kind, float eps,
+                                             const bool (&in)[CH], Get get) {
   if (kind == kNormNone) return make_float2(0.f, 1.f);
   if (kind == kNormRms) {
     float q = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = row_index<true>(g, c, 0);
-      if (i < n) {
-        float v[8];
-        get(c, i, v);
+      Oct v;
+      get(c, v);
+      float2 s = mul2(v.p[0], v.p[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q = fmaf(v[j], v[j], q);
-      }
+      for (int j = 1; j < 4; ++j) s = fma2(v.p[j], v.p[j], s);
+      q += in[c] ? s.x + s.y : 0.f;
     }
     return make_float2(0.f, rsqrtf(row_sum(g, q) / n + eps));
   }
-  // as row_moments (rows.cuh), over chunks that are read again
+  // as row_moments (rows.cuh)
   float s = 0.f, cnt = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = row_index<true>(g, c, 0);
-    if (i < n) {
-      float v[8];
-      get(c, i, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[j];
-      cnt += 8.f;
-    }
+    Oct v;
+    get(c, v);
+    const float2 t = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
+    s += in[c] ? t.x + t.y : 0.f;
+    cnt += in[c] ? 8.f : 0.f;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -232,18 +264,22 @@ __device__ __forceinline__ float2 row_stat(RowGroup& g, int n, int kind, float e
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = row_index<true>(g, c, 0);
-    if (i < n) {
-      float v[8];
-      get(c, i, v);
+    Oct v;
+    get(c, v);
+    float2 d = add2(v.p[0], pair(-mean));
+    float2 t = mul2(d, d);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q = fmaf(v[j] - mean, v[j] - mean, q);
+    for (int j = 1; j < 4; ++j) {
+      d = add2(v.p[j], pair(-mean));
+      t = fma2(d, d, t);
     }
+    q += in[c] ? t.x + t.y : 0.f;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
   const float2 mv = combine_moments(g, mean, q, cnt, n);
-  return make_float2(mv.x, rsqrtf(mv.y + eps));
+  const float r = rsqrtf(mv.y + eps);
+  return make_float2(-mv.x * r, r);
 }
 
 template <class Tx, class Ty, int CH>
@@ -254,10 +290,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
   const int rows_threads = s.groups * s.threads;
   const int64_t b = blockIdx.y;
   const int C = a.C;
-  float* gain = reinterpret_cast<float*>(sm);                    // branch_scale gate post_weight
-  float* pbias = gain + (s.has_gain ? C : 0);                    // branch_scale gate post_bias
-  float* va = pbias + (s.has_post_bias ? C : 0);                 // pre_weight (1 + scale)
-  float* vb = va + (s.has_a ? C : 0);                            // pre_bias (1 + scale) + shift
+  const int len = (C + 255) & ~255;                                // of a folded vector
+  float* gain = reinterpret_cast<float*>(sm);                      // branch_scale gate post_weight
+  float* pbias = gain + (s.has_gain ? len : 0);                    // branch_scale gate post_bias
+  float* va = pbias + (s.has_post_bias ? len : 0);                 // pre_weight (1 + scale)
+  float* vb = va + (s.has_a ? len : 0);                            // pre_bias (1 + scale) + shift
   if (threadIdx.x == 0) {
     for (int i = 0; i < s.stages; ++i) {
       mbar_init(&ctl->full[i], 1);
@@ -274,10 +311,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     const float gt = a.gate ? mod(a.gate, b * a.gate_b, i) : 1.f;
     const float sc = a.mscale ? 1.f + mod(a.mscale, b * a.scale_b, i) : 1.f;
     const float sh = a.shift ? mod(a.shift, b * a.shift_b, i) : 0.f;
-    if (s.has_gain) gain[i] = a.branch_scale * gt * (a.post_weight ? __ldg(a.post_weight + i) : 1.f);
-    if (s.has_post_bias) pbias[i] = a.branch_scale * gt * __ldg(a.post_bias + i);
-    if (s.has_a) va[i] = sc * (a.pre_weight ? __ldg(a.pre_weight + i) : 1.f);
-    if (s.has_b) vb[i] = fmaf(a.pre_bias ? __ldg(a.pre_bias + i) : 0.f, sc, sh);
+    const int at = folded_at(i);
+    if (s.has_gain) gain[at] = a.branch_scale * gt * (a.post_weight ? __ldg(a.post_weight + i) : 1.f);
+    if (s.has_post_bias) pbias[at] = a.branch_scale * gt * __ldg(a.post_bias + i);
+    if (s.has_a) va[at] = sc * (a.pre_weight ? __ldg(a.pre_weight + i) : 1.f);
+    if (s.has_b) vb[at] = fmaf(a.pre_bias ? __ldg(a.pre_bias + i) : 0.f, sc, sh);
   }
   __syncthreads();
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
@@ -308,81 +346,112 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
   const int group = threadIdx.x / s.threads;
   RowGroup g{static_cast<int>(threadIdx.x) - group * s.threads, s.threads, 1 + group,
              reinterpret_cast<RowReduce*>(sm + s.off_red) + group, 0};
-  for (int64_t i = group;; i += s.groups) {
-    const int64_t t = blockIdx.x + i * step;
-    if (t >= a.N) break;
-    const int st = static_cast<int>(i % s.stages);
+  // chunks past the row's end read its last one again and neither count nor store
+  int at[CH];
+  bool in[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int k = row_index<true>(g, c, 0);
+    in[c] = k < C;
+    at[c] = in[c] ? k : C - 8;
+  }
+  uint32_t st = group % s.stages, round = group / s.stages;
+  for (int64_t t = blockIdx.x + group * step; t < a.N; t += s.groups * step) {
     // the whole group goes on or none of it
-    if (!g.all(mbar_wait(&ctl->full[st], (i / s.stages) & 1, wc))) break;
+    if (!g.all(mbar_wait(&ctl->full[st], round & 1, wc))) break;
     const Tx* xs = reinterpret_cast<const Tx*>(sm + s.off_stage + st * stage_bytes);
     const Ty* ys = reinterpret_cast<const Ty*>(sm + s.off_stage + st * stage_bytes + s.x_bytes);
-    float h[CH][8];
+    Oct h[CH];
     if (s.y_bytes) {
-      const float2 mr = row_stat<CH>(g, C, a.post, a.eps, [&](int, int k, float v[8]) { smem8(ys, k, v); });
-      Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
+      const float2 mr = row_affine<CH>(g, C, a.post, a.eps, in,
+                                       [&](int c, Oct& v) { smem8(ys + at[c], v); });
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        const int k = row_index<true>(g, c, 0);
-        if (k < C) {
-          float v[8], m[8];
-          smem8(ys, k, v);
+        smem8(ys + at[c], h[c]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = (v[j] - mr.x) * mr.y;
-          if (s.has_gain) {
-            smem8(gain, k, m);
+        for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(h[c].p[j], pair(mr.y), pair(mr.x));
+      }
+      if (s.has_gain) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= m[j];
-          }
-          if (s.has_post_bias) {
-            smem8(pbias, k, m);
+        for (int c = 0; c < CH; ++c) {
+          Oct m;
+          folded8(gain, at[c], m);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += m[j];
-          }
-          smem8(xs, k, h[c]);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], a.residual_scale, v[j]);
-          if (a.h) store8<true>(g, ho, C, c, h[c]);
+          for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], m.p[j]);
         }
+      }
+      if (s.has_post_bias) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          Oct m;
+          folded8(pbias, at[c], m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Oct x;
+        smem8(xs + at[c], x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(x.p[j], pair(a.residual_scale), h[c].p[j]);
+      }
+      mbar_arrive(&ctl->empty[st]);
+      if (a.h) {
+        Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+          if (in[c]) put8(ho + at[c], h[c]);
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int k = row_index<true>(g, c, 0);
-        if (k < C) smem8(xs, k, h[c]);
-      }
+      for (int c = 0; c < CH; ++c) smem8(xs + at[c], h[c]);
+      mbar_arrive(&ctl->empty[st]);
     }
-    mbar_arrive(&ctl->empty[st]);
+    st += s.groups;
+    while (st >= static_cast<uint32_t>(s.stages)) st -= s.stages, ++round;
     if (!a.z) continue;
-    const float2 mr = row_stat<CH>(g, C, a.pre, a.eps, [&](int c, int, float v[8]) {
+    const float2 mr =
+        row_affine<CH>(g, C, a.pre, a.eps, in, [&](int c, Oct& v) { v = h[c]; });
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = h[c][j];
-    });
-    const int64_t o = b * a.z_b + t * a.z_n;
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int k = row_index<true>(g, c, 0);
-      if (k < C) {
-        float m[8];
+      for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(h[c].p[j], pair(mr.y), pair(mr.x));
+    if (s.has_a) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] = (h[c][j] - mr.x) * mr.y;
-        if (s.has_a) {
-          smem8(va, k, m);
+      for (int c = 0; c < CH; ++c) {
+        Oct m;
+        folded8(va, at[c], m);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[c][j] *= m[j];
-        }
-        if (s.has_b) {
-          smem8(vb, k, m);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[c][j] += m[j];
-        }
-        store_z8<true>(g, a, o, c, h[c]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] = 0.f;
+        for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], m.p[j]);
       }
     }
-    if (a.z_type == kTypeInt8) {
-      const float sc = store_codes<CH, true>(g, h, C, static_cast<int8_t*>(a.z) + o);
+    if (s.has_b) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Oct m;
+        folded8(vb, at[c], m);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
+      }
+    }
+    const int64_t o = b * a.z_b + t * a.z_n;
+    if (a.z_type == kTypeBf16) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (in[c]) put8(static_cast<__nv_bfloat16*>(a.z) + o + at[c], h[c]);
+    } else if (a.z_type == kTypeFp32) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (in[c]) put8(static_cast<float*>(a.z) + o + at[c], h[c]);
+    } else {
+      float x[CH][8];
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[c][j] = in[c] ? (j & 1 ? h[c].p[j >> 1].y : h[c].p[j >> 1].x) : 0.f;
+      const float sc = store_codes<CH, true>(g, x, C, static_cast<int8_t*>(a.z) + o);
       if (g.tid == 0) a.z_scale[b * a.N + t] = sc;
     }
   }
@@ -395,7 +464,6 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   const bool token = (a.gate && a.gate_n) || (a.mscale && a.scale_n) || (a.shift && a.shift_n);
   if (token) return false;
   const int per = 148 / a.B > 0 ? 148 / a.B : 1;
-  if (a.N < 4 * per || a.B > 65535) return false;
   s->x_bytes = static_cast<uint32_t>(a.C) * (x_fp32 ? 4 : 2);
   s->y_bytes = a.y ? static_cast<uint32_t>(a.C) * (a.y_fp32 ? 4 : 2) : 0;
   if (s->x_bytes + s->y_bytes < 4096) return false;
@@ -405,11 +473,15 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   if (s->threads > kRingThreads - 32) return false;
   s->groups = (kRingThreads - 32) / s->threads;
   if (s->groups > kMaxGroups) s->groups = kMaxGroups;
+  // at least four rows a group, or filling the vectors does not pay: 2,000 rows of 1,024 take
+  // 12.3 us here and 8.3 us with a CTA a row
+  if (a.N < 4 * per * s->groups || a.B > 65535) return false;
   s->has_gain = a.y && (a.gate || a.post_weight || a.branch_scale != 1.f);
   s->has_post_bias = a.y && a.post_bias;
   s->has_a = a.z && (a.mscale || a.pre_weight);
   s->has_b = a.z && (a.shift || a.pre_bias);
-  const uint32_t vectors = (s->has_gain + s->has_post_bias + s->has_a + s->has_b) * a.C * 4u;
+  const uint32_t vectors =
+      (s->has_gain + s->has_post_bias + s->has_a + s->has_b) * ((a.C + 255) & ~255) * 4u;
   s->off_stage = (vectors + 127) & ~127u;
   const uint32_t fixed = s->groups * static_cast<uint32_t>(sizeof(RowReduce)) + sizeof(RingCtl) + 16;
   const uint32_t stage = s->x_bytes + s->y_bytes;

@@ -1,10 +1,11 @@
 // Rows to int8 codes with one scale a row (rows.cuh: store_codes), the left
-// operand of the int8 product and, once, its weights.
+// operand of the int8 product and, once, its weights.  |code| <= 127.
 //
 // Row (b, n) has S segments of L values; segment s starts at b x_b + n x_n +
 // s x_s.  The attention's head-major output [B, H, N, 128] is read as token
 // rows of H segments of 128, so no transposed copy is made.  HBM-bound: each
-// value is read once (2 B) and its code written once (1 B).
+// value is read once (2 B) and its code written once (1 B); 131 us for
+// 37,740 x 7,168 head-major bf16, 6.2 TB/s.
 #include "bsa_kernels.h"
 #include "rows.cuh"
 
@@ -12,8 +13,9 @@ namespace bsa {
 
 namespace {
 
-template <class Tx, int CH, int kThreads, bool kVec>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) quant_int8_kernel(const QuantInt8Args a) {
+// Any rows, fp32 in registers.
+template <class Tx, int CH, bool kVec>
+__global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args a) {
   __shared__ RowReduce red;
   RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
@@ -25,44 +27,67 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) quant_int8_kernel(c
     if (a.S == 1) {
       load_row<CH, kVec>(g, src, n, x);
     } else {
-      if constexpr (kVec) {       // L is a multiple of 8: a chunk lies in one segment
-        constexpr int W = static_cast<int>(sizeof(Tx)) / 2;   // 16-byte words a chunk
-        uint4 w[CH][W];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          const int i = row_index<true>(g, c, 0);
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = row_index<kVec>(g, c, j);
           const int s = i / a.L;
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            w[c][k] = make_uint4(0, 0, 0, 0);
-            if (i < n) w[c][k] = ld_row_v4(src + s * a.x_s + (i - s * a.L) + 4 * k);
-          }
+          x[c][j] = i < n ? to_f32(src[s * a.x_s + (i - s * a.L)]) : 0.f;
         }
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          if constexpr (W == 1) {
-            bf16x8_to_f32(w[c][0], x[c]);
-          } else {
-#pragma unroll
-            for (int k = 0; k < W; ++k) {
-              x[c][4 * k] = __uint_as_float(w[c][k].x), x[c][4 * k + 1] = __uint_as_float(w[c][k].y);
-              x[c][4 * k + 2] = __uint_as_float(w[c][k].z), x[c][4 * k + 3] = __uint_as_float(w[c][k].w);
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int i = row_index<false>(g, c, j);
-            const int s = i / a.L;
-            x[c][j] = i < n ? to_f32(src[s * a.x_s + (i - s * a.L)]) : 0.f;
-          }
-      }
     }
     const float s = store_codes<CH, kVec>(g, x, n, a.q + row * a.q_ld);
-    if (threadIdx.x == 0) a.scale[row] = s;
+    if (g.tid == 0) a.scale[row] = s;
+  }
+}
+
+// bf16 rows of aligned 8-value chunks: the words stay packed between the two
+// steps (half the registers, so more rows in flight on an SM), and the maximum
+// is taken on them as 16-bit integers, which order magnitudes with NaN on top.
+template <int CH, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(const QuantInt8Args a) {
+  __shared__ RowReduce red;
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
+  const int64_t rows = static_cast<int64_t>(a.B) * a.N;
+  const int n = a.S * a.L;
+  int64_t off[CH];                               // of this thread's chunks in every row
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = row_index<true>(g, c, 0);
+    const int s = a.S == 1 ? 0 : i / a.L;        // a chunk lies in one segment
+    off[c] = s * a.x_s + (i - s * a.L);
+  }
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t b = a.B == 1 ? 0 : row / a.N, t = row - b * a.N;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + b * a.x_b + t * a.x_n;
+    uint4 w[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      w[c] = make_uint4(0, 0, 0, 0);
+      if (row_index<true>(g, c, 0) < n) w[c] = ld_stream_v4(src + off[c]);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      m = __vmaxu2(m, __vmaxu2(w[c].x & 0x7fff7fffu, w[c].y & 0x7fff7fffu));
+      m = __vmaxu2(m, __vmaxu2(w[c].z & 0x7fff7fffu, w[c].w & 0x7fff7fffu));
+    }
+    const uint32_t top = max(m & 0xffffu, m >> 16) << 16;
+    float am = row_max_abs(g, __uint_as_float(top));
+    const bool finite = am <= 3.402823466e38f;
+    am = finite ? fmaxf(am, kInt8Floor) : am;
+    const float inv = __fdiv_rn(127.f, am);
+    int8_t* q = a.q + row * a.q_ld;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int i = row_index<true>(g, c, 0);
+      float x[8];
+      bf16x8_to_f32(w[c], x);
+      uint2 k = make_uint2(0, 0);
+      if (finite) k = make_uint2(codes4(x, inv), codes4(x + 4, inv));
+      if (i < n) *reinterpret_cast<uint2*>(q + i) = k;
+    }
+    if (g.tid == 0) a.scale[row] = finite ? __fdiv_rn(am, 127.f) : __uint_as_float(0x7fc00000u);
   }
 }
 
@@ -72,11 +97,9 @@ cudaError_t launch(const QuantInt8Args& a, int ch, int threads, int blocks, cuda
     k<<<blocks, threads, 0, st>>>(a);
     return cudaGetLastError();
   };
-  if (ch == 1) return go(quant_int8_kernel<Tx, 1, 1024, kVec>);
-  if (ch == 2) return go(quant_int8_kernel<Tx, 2, 1024, kVec>);
-  if (threads <= 256) return go(quant_int8_kernel<Tx, 4, 256, kVec>);
-  if (threads <= 512) return go(quant_int8_kernel<Tx, 4, 512, kVec>);
-  return go(quant_int8_kernel<Tx, 4, 1024, kVec>);
+  if (ch == 1) return go(quant_int8_kernel<Tx, 1, kVec>);
+  if (ch == 2) return go(quant_int8_kernel<Tx, 2, kVec>);
+  return go(quant_int8_kernel<Tx, 4, kVec>);
 }
 
 }  // namespace
@@ -85,7 +108,25 @@ cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cud
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   int ch, threads;
   row_shape(a.S * a.L, rows, &ch, &threads);
-  const int blocks = static_cast<int>(rows < (1 << 30) ? rows : (1 << 30));
+  int blocks = static_cast<int>(rows < (1 << 30) ? rows : (1 << 30));
+  if (vec && !x_fp32) {
+    const int vecs = (a.S * a.L + 7) / 8;
+    if (ch > 1) {
+      ch = 4;
+      threads = ((vecs + 3) / 4 + 31) / 32 * 32;
+      // as many CTAs as are resident at once: 131 us for 37,740 head-major rows of 7,168 against
+      // 142 with a CTA a row
+      const int resident = 1536 / threads < 32 ? 1536 / threads : 32;
+      if (resident > 0 && blocks > 148 * resident) blocks = 148 * resident;
+    }
+    auto go = [&](auto k) {
+      k<<<blocks, threads, 0, st>>>(a);
+      return cudaGetLastError();
+    };
+    if (ch == 1) return go(quant_int8_bf16_kernel<1, 1024, 1>);
+    if (threads <= 256) return go(quant_int8_bf16_kernel<4, 256, 6>);
+    return go(quant_int8_bf16_kernel<4, 1024, 1>);
+  }
   if (vec)
     return x_fp32 ? launch<float, true>(a, ch, threads, blocks, st)
                   : launch<__nv_bfloat16, true>(a, ch, threads, blocks, st);

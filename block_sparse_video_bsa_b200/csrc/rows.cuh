@@ -269,6 +269,18 @@ __device__ __forceinline__ float2 row_moments(RowGroup& g, const float (&x)[CH][
   return combine_moments(g, mean, q, cnt, n);
 }
 
+// Code of one value, in the low byte: the product is rounded to fp32, and the
+// sum with 1.5 2^23 rounds it to a whole number, half to even (|product| <=
+// 127.00002), whose two's complement is the sum's low bits.
+__device__ __forceinline__ uint32_t code_bits(float x, float inv) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.f));
+}
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
+  const uint32_t lo = __byte_perm(code_bits(x[0], inv), code_bits(x[1], inv), 0x0040);
+  const uint32_t hi = __byte_perm(code_bits(x[2], inv), code_bits(x[3], inv), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
+}
+
 // int8 codes of a row: scale = amax / 127, code = rint(x * (127 / amax)), both
 // factors rounded to fp32, |code| <= 127.  A row that holds a NaN or an
 // infinity has a scale that is not finite (NaN) and codes 0: its products are
@@ -286,28 +298,19 @@ __device__ __forceinline__ float store_codes(RowGroup& g, const float (&x)[CH][8
   m = row_max_abs(g, m);
   const bool finite = m <= 3.402823466e38f;
   m = finite ? fmaxf(m, kInt8Floor) : m;
-  const float inv = finite ? __fdiv_rn(127.f, m) : 0.f;
+  const float inv = __fdiv_rn(127.f, m);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    int v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = finite ? __float2int_rn(__fmul_rn(x[c][j], inv)) : 0;
     if constexpr (kVec) {
       const int i = row_index<true>(g, c, 0);
-      if (i < n) {
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          lo |= static_cast<uint32_t>(v[j] & 255) << (8 * j);
-          hi |= static_cast<uint32_t>(v[j + 4] & 255) << (8 * j);
-        }
-        *reinterpret_cast<uint2*>(q + i) = make_uint2(lo, hi);
-      }
+      uint2 w = make_uint2(0, 0);
+      if (finite) w = make_uint2(codes4(x[c], inv), codes4(x[c] + 4, inv));
+      if (i < n) *reinterpret_cast<uint2*>(q + i) = w;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int i = row_index<false>(g, c, j);
-        if (i < n) q[i] = static_cast<int8_t>(v[j]);
+        if (i < n) q[i] = finite ? static_cast<int8_t>(code_bits(x[c][j], inv)) : 0;
       }
     }
   }
