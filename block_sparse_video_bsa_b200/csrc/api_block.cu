@@ -341,7 +341,7 @@ int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   int box_a, box_w;
-  bsa::linear_int8_boxes(p->M, p->N, p->K, &box_a, &box_w);
+  bsa::linear_int8_boxes(p->M, p->N, &box_a, &box_w);
   CUtensorMap ma, mw;
   if (!map(&ma, a, p->M, p->lda, box_a) || !map(&mw, w, p->N, p->ldw, box_w))
     return BSA_ERR_UNSUPPORTED;

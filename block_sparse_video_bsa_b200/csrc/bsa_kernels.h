@@ -231,7 +231,7 @@ struct LinearInt8Args {
   int* dev_status;
 };
 // Rows of the tensor maps' boxes (128 bytes wide) of the tokens and the weights.
-void linear_int8_boxes(int M, int N, int K, int* box_a, int* box_w);
+void linear_int8_boxes(int M, int N, int* box_a, int* box_w);
 cudaError_t launch_linear_int8(const LinearInt8Args& a, const CUtensorMap& ma,
                                const CUtensorMap& mw, cudaStream_t st);
 

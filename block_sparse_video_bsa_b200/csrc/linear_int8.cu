@@ -6,14 +6,13 @@
 // K <= 32,768 (K 127^2 < 2^31), so neither the order of K nor a split of it
 // changes a bit; the scales, the bias and one rounding follow in fp32.
 //
-// One CTA per SM walks over output tiles.  Warp 4 brings 128-byte K slices of
-// both operands into a ring of shared-memory stages by TMA (128-byte swizzle;
-// rows and bytes past an operand's end read as zero), warp 5 issues the MMAs,
-// warps 0-3 turn a finished accumulator into output rows while the next tile
-// accumulates into the other half of TMEM.
-//
-// The operand on the MMA's M side (128 rows, one TMEM lane each) is the tokens
-// for many tokens, the weights for few (kSwap).
+// Two kernels, both with TMA for the operands (128-byte K slices, 128-byte
+// swizzle; rows and bytes past an operand's end read as zero), a ring of
+// shared-memory stages, one thread that issues the MMAs and warps that turn
+// accumulators into output:
+//   linear_int8_pair_kernel  many tokens: CTA pairs, tokens on the MMA's M side;
+//   linear_int8_few_kernel   up to 64 tokens: the weights on the M side, K split
+//                            over a cluster.
 #include "bsa_device.cuh"
 #include "bsa_kernels.h"
 
@@ -21,24 +20,8 @@ namespace bsa {
 
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kSlice = 128;                 // bytes of K a stage
 constexpr int kRowTile = 128;
-
-template <int kCols>
-struct LinearSmem {
-  static constexpr int kRing = kCols >= 128 ? 6 : (kCols >= 64 ? 8 : 10);
-  static constexpr uint32_t kA = kRowTile * kSlice, kB = kCols * kSlice;
-  static constexpr uint32_t kCtl = kRing * (kA + kB);
-  static constexpr uint32_t kBytes = kCtl + 256 + 1024;   // control, base alignment
-};
-
-struct LinearCtl {
-  uint64_t full[10], empty[10], acc_full[2], acc_empty[2];
-  uint32_t tmem_base;
-  int abort_flag;
-};
-static_assert(sizeof(LinearCtl) <= 256, "control block");
 
 // Tile order: columns of `kGroup` row tiles at a time, so that tiles in flight
 // share operand rows in L2.
@@ -52,34 +35,72 @@ __device__ __forceinline__ void tile_of(int64_t t, int row_tiles, int col_tiles,
   *c = static_cast<int>(in / rows);
 }
 
-template <int kCols, bool kSwap>
-__global__ void __launch_bounds__(kThreads, 1) linear_int8_kernel(
-    const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_c,
-    const LinearInt8Args a, int row_tiles, int col_tiles) {
-  using S = LinearSmem<kCols>;
+// ------------------------------------------------------------ few tokens
+
+// 128 channels x kCols tokens a tile, the weights on the MMA's M side.  What
+// bounds it is the stream of weights, so a cluster of CTAs splits K: each sums
+// its share of the slices, keeps the int32 partial sums in shared memory, and
+// the cluster adds them over distributed shared memory (whole numbers: the
+// order does not matter).  No workspace, no atomics.
+constexpr int kFewThreads = 192;     // warps 0-3 epilogue, 4 producer, 5 MMA
+constexpr int kMaxSplit = 8;
+
+template <int kCols>
+struct FewSmem {
+  static constexpr uint32_t kA = kRowTile * kSlice, kB = kCols * kSlice;
+  static constexpr uint32_t kSums = kCols * kRowTile * 4;
+  // two CTAs an SM
+  static constexpr uint32_t kRoom = 111 * 1024 - 512 - 1024 - kSums;
+  static constexpr int kRing = static_cast<int>(kRoom / (kA + kB));
+  static constexpr uint32_t kOffSums = kRing * (kA + kB);
+  static constexpr uint32_t kCtl = kOffSums + kSums;
+  static constexpr uint32_t kBytes = kCtl + 512 + 1024;   // control, base alignment
+};
+struct FewCtl {
+  uint64_t full[8], empty[8], acc_full;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(FewCtl) <= 512 && FewSmem<16>::kRing <= 8 && FewSmem<64>::kRing <= 8,
+              "control block");
+
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int kCols>
+__global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
+    const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+    const LinearInt8Args a, int split) {
+  using S = FewSmem<kCols>;
   constexpr int kRing = S::kRing;
   constexpr uint32_t kAccCols = kCols < 32 ? 32 : kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  LinearCtl* ctl = reinterpret_cast<LinearCtl*>(sm + S::kCtl);
+  FewCtl* ctl = reinterpret_cast<FewCtl*>(sm + S::kCtl);
+  int32_t* sums = reinterpret_cast<int32_t*>(sm + S::kOffSums);   // [kCols][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t tiles = static_cast<int64_t>(row_tiles) * col_tiles;
+  const int r = blockIdx.x / split, rank = blockIdx.x % split;    // one cluster a row tile
   const int slices = (a.K + kSlice - 1) / kSlice;
+  const int k0 = static_cast<int>(static_cast<int64_t>(slices) * rank / split);
+  const int k1 = static_cast<int>(static_cast<int64_t>(slices) * (rank + 1) / split);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->acc_full[i], 1);
-      mbar_init(&ctl->acc_empty[i], 128);
-    }
+    mbar_init(&ctl->acc_full, 1);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 5) {
-    tmem_alloc(&ctl->tmem_base, 2 * kAccCols);
+    tmem_alloc(&ctl->tmem_base, kAccCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -89,118 +110,163 @@ __global__ void __launch_bounds__(kThreads, 1) linear_int8_kernel(
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
 
   if (warp == 4 && lane == 0) {
-    prefetch_tensormap(&map_r);
-    prefetch_tensormap(&map_c);
-    int64_t seq = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      int r, c;
-      tile_of(t, row_tiles, col_tiles, &r, &c);
-      for (int k = 0; k < slices; ++k, ++seq) {
-        const int stage = static_cast<int>(seq % kRing);
-        if (seq >= kRing && !mbar_wait(&ctl->empty[stage], ((seq / kRing) - 1) & 1, wc)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(&ctl->full[stage], S::kA + S::kB);
-        tma_load_2d(sm + stage * (S::kA + S::kB), &map_r, &ctl->full[stage], k * kSlice,
-                    r * kRowTile);
-        tma_load_2d(sm + stage * (S::kA + S::kB) + S::kA, &map_c, &ctl->full[stage], k * kSlice,
-                    c * kCols);
-      }
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_a);
+    uint32_t stage = 0, round = 0;
+    for (int k = k0; k < k1; ++k) {
+      if (round > 0 && !mbar_wait(&ctl->empty[stage], (round - 1) & 1, wc)) break;
+      mbar_arrive_expect_tx(&ctl->full[stage], S::kA + S::kB);
+      uint8_t* dst = sm + stage * (S::kA + S::kB);
+      tma_load_2d(dst, &map_w, &ctl->full[stage], k * kSlice, r * kRowTile);
+      tma_load_2d(dst + S::kA, &map_a, &ctl->full[stage], k * kSlice, 0);
+      if (++stage == kRing) stage = 0, ++round;
     }
     // every issued load has landed before the CTA exits
-    for (int64_t k = (seq > kRing ? seq - kRing : 0); k < seq; ++k)
+    const int issued = static_cast<int>(round) * kRing + static_cast<int>(stage);
+    for (int k = (issued > kRing ? issued - kRing : 0); k < issued; ++k)
       mbar_wait(&ctl->full[k % kRing], (k / kRing) & 1, wc);
   } else if (warp == 5 && lane == 0) {
     const uint32_t id = idesc_s8_s32(kRowTile, kCols);
-    int64_t seq = 0;
-    int it = 0;
+    uint32_t stage = 0, round = 0;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++it) {
-      const int buf = it & 1;
-      if (it >= 2 && !mbar_wait(&ctl->acc_empty[buf], ((it >> 1) - 1) & 1, wc)) break;
-      tc_fence_after();
-      for (int k = 0; k < slices; ++k, ++seq) {
-        const int stage = static_cast<int>(seq % kRing);
-        if (!mbar_wait(&ctl->full[stage], (seq / kRing) & 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t ra = smem_u32(sm + stage * (S::kA + S::kB));
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_s8_ss(tmem + buf * kAccCols, smem_desc_sw128(ra + kk * 32, 16, 1024),
-                    smem_desc_sw128(ra + S::kA + kk * 32, 16, 1024), id, (k | kk) ? 1u : 0u);
-        mma_commit(&ctl->empty[stage]);
+    for (int k = k0; k < k1; ++k) {
+      if (!mbar_wait(&ctl->full[stage], round & 1, wc)) {
+        ok = false;
+        break;
       }
-      if (ok) mma_commit(&ctl->acc_full[buf]);
-    }
-  } else if (warp < 4) {
-    int it = 0;
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
-      const int buf = it & 1;
-      int r, c;
-      tile_of(t, row_tiles, col_tiles, &r, &c);
-      if (!mbar_wait(&ctl->acc_full[buf], (it >> 1) & 1, wc)) break;
       tc_fence_after();
-      const int row = r * kRowTile + warp * 32 + lane;   // a token, or a channel (kSwap)
-      const uint32_t src = tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * kAccCols;
-      const bool row_ok = row < (kSwap ? a.N : a.M);
-      const float rs = row_ok ? __ldg((kSwap ? a.w_scale : a.a_scale) + row) : 0.f;
-      const float rb = kSwap && row_ok && a.bias ? __ldg(a.bias + row) : 0.f;
+      const uint32_t ra = smem_u32(sm + stage * (S::kA + S::kB));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_s8_ss(tmem, smem_desc_sw128(ra + kk * 32, 16, 1024),
+                  smem_desc_sw128(ra + S::kA + kk * 32, 16, 1024), id, (k > k0 || kk) ? 1u : 0u);
+      mma_commit(&ctl->empty[stage]);
+      if (++stage == kRing) stage = 0, ++round;
+    }
+    if (ok) mma_commit(&ctl->acc_full);
+  } else if (warp < 4) {
+    // this share's sums, [token][channel]
+    if (mbar_wait(&ctl->acc_full, 0, wc)) {
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t src = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
       for (int c0 = 0; c0 < kCols; c0 += 8) {
         uint32_t v[8];
         tmem_ld8(src + c0, v);
         tmem_wait_ld();
-        const int col0 = c * kCols + c0;
-        float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = col0 + j;
-          const bool in = col < (kSwap ? a.M : a.N);
-          const float cs = in ? __ldg((kSwap ? a.a_scale : a.w_scale) + col) : 0.f;
-          const float cb = !kSwap && in && a.bias ? __ldg(a.bias + col) : rb;
-          // (sum * a_scale[m]) * w_scale[n] + bias, the same in both orders
-          const float sum = static_cast<float>(static_cast<int32_t>(v[j]));
-          o[j] = kSwap ? fmaf(sum * cs, rs, cb) : fmaf(sum * rs, cs, cb);
-        }
-        if (!row_ok) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int col = col0 + j;
-          if (col >= (kSwap ? a.M : a.N)) break;
-          const int64_t at = kSwap ? col * a.ldo + row : row * a.ldo + col;
-          if (a.out_fp32)
-            static_cast<float*>(a.out)[at] = o[j];
-          else
-            static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o[j]);
-        }
+        for (int j = 0; j < 8; ++j)
+          sums[(c0 + j) * kRowTile + warp * 32 + lane] = static_cast<int32_t>(v[j]);
       }
-      tc_fence_before();
-      mbar_arrive(&ctl->acc_empty[buf]);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_dealloc(tmem, 2 * kAccCols);
+  if (split > 1) cluster_sync();
+  if (warp < 4) {
+    // warp w of rank q finishes tokens q + split (w + 4 i), four neighbouring channels a lane
+    const int ch = r * kRowTile + 4 * lane;
+    float ws[4], cb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ws[j] = ch + j < a.N ? __ldg(a.w_scale + ch + j) : 0.f;
+      cb[j] = ch + j < a.N && a.bias ? __ldg(a.bias + ch + j) : 0.f;
+    }
+    for (int m = rank + split * warp; m < kCols && m < a.M; m += 4 * split) {
+      int4 sum = make_int4(0, 0, 0, 0);
+      const int32_t* at = sums + m * kRowTile + 4 * lane;
+      if (split == 1) {
+        sum = *reinterpret_cast<const int4*>(at);
+      } else {
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q) {
+          if (q < split) {
+            const int4 p = ld_cluster_v4(map_to_rank(at, q));
+            sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
+          }
+        }
+      }
+      const float rs = __ldg(a.a_scale + m);
+      const float o[4] = {fmaf(static_cast<float>(sum.x) * rs, ws[0], cb[0]),
+                          fmaf(static_cast<float>(sum.y) * rs, ws[1], cb[1]),
+                          fmaf(static_cast<float>(sum.z) * rs, ws[2], cb[2]),
+                          fmaf(static_cast<float>(sum.w) * rs, ws[3], cb[3])};
+      const int64_t to = m * a.ldo + ch;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (ch + j < a.N) {
+          if (a.out_fp32)
+            static_cast<float*>(a.out)[to + j] = o[j];
+          else
+            static_cast<__nv_bfloat16*>(a.out)[to + j] = __float2bfloat16_rn(o[j]);
+        }
+      }
+    }
+  }
+  if (split > 1) cluster_sync();   // the peers have read this CTA's sums
+  if (warp == 5) {
+    __syncwarp();
+    tmem_dealloc(tmem, kAccCols);
+  }
+}
+
+// CTAs a cluster: as many as keep all clusters on the GPU at once with room to
+// place them, 224 CTAs (1 x 7,168 x 7,168, 56 row tiles: 18.3 us unsplit, 14.4
+// in 2, 13.7 in 3 or 4, 15.1 in 5, 18 in 6; 168 row tiles: 29.0 us unsplit,
+// 34.9 in 2).
+int few_split(int row_tiles, int slices) {
+  int s = row_tiles < 224 ? 224 / row_tiles : 1;
+  if (s > kMaxSplit) s = kMaxSplit;
+  return s < slices ? s : slices;
+}
+
+template <int kCols>
+cudaError_t go_few(const LinearInt8Args& a, const CUtensorMap& mw, const CUtensorMap& ma,
+                   cudaStream_t st) {
+  using S = FewSmem<kCols>;
+  auto* kernel = linear_int8_few_kernel<kCols>;
+  static std::atomic<bool> done[64];
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const int rt = (a.N + kRowTile - 1) / kRowTile;
+  const int split = few_split(rt, (a.K + kSlice - 1) / kSlice);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split * rt);
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, a, split);
 }
 
 // ------------------------------------------------------------ CTA pairs
 
 // 256 tokens x kN channels a tile, computed by two CTAs as one MMA of 256 x kN
 // x 32: each brings its 128 tokens and half of the channels, so an SM reads
-// 128 + kN / 2 rows for 128 x kN products instead of 128 + kN.
+// 128 + kN / 2 rows for 128 x kN products instead of 128 + kN (one CTA of 128 x
+// 128 took 3,650 us for 37,740 x 7,168 x 7,168, where shared-memory bandwidth
+// bounds it; pairs of 256 x 256 take 1,256 to 1,347 us, 2.9 to 3.1 POP/s with
+// the clock under the power cap).  Persistent: warp 8 loads, warp 9 of CTA 0
+// issues, warps 0-7 finish a tile while the next accumulates into the other
+// half of TMEM.
 constexpr int kPairThreads = 320;    // warps 0-7 epilogue, 8 producer, 9 MMA
 constexpr int kPairRows = 256;
 
 template <int kN>
 struct PairSmem {
   static constexpr uint32_t kA = 128 * kSlice, kB = kN / 2 * kSlice;
-  static constexpr int kRing = static_cast<int>((226 * 1024 - 1024 - 512) / (kA + kB));
-  static constexpr uint32_t kCtl = kRing * (kA + kB);
+  static constexpr uint32_t kStaging = 8 * 32 * 33 * 4;     // a 32 x 32 block a warp
+  static constexpr int kRing = static_cast<int>((227 * 1024 - 1024 - 512 - kStaging) / (kA + kB));
+  static constexpr uint32_t kOffStaging = kRing * (kA + kB);
+  static constexpr uint32_t kCtl = kOffStaging + kStaging;
   static constexpr uint32_t kBytes = kCtl + 512 + 1024;
 };
 struct PairCtl {
@@ -216,56 +282,69 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// 32 output values of row `row`, columns col .. col + 31, from int32 sums.
-__device__ __forceinline__ void finish32(const LinearInt8Args& a, int64_t row, int col, float rs,
-                                         const uint32_t (&v)[32], bool wide) {
-  if (wide && col + 32 <= a.N) {
+// 32 output values of row `row`, columns col .. col + 31, from int32 sums: one
+// row a thread, whole 32-byte sectors.
+__device__ __forceinline__ void finish_row(const LinearInt8Args& a, int64_t row, int col, float rs,
+                                           const uint32_t (&v)[32]) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      float o[16];
+  for (int q = 0; q < 2; ++q) {
+    float o[16];
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col + 16 * q + j));
-        float4 cb = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (a.bias) cb = __ldg(reinterpret_cast<const float4*>(a.bias + col + 16 * q + j));
-        const int at = 16 * q + j;
-        const float2 p0 = mul2(make_float2(static_cast<int32_t>(v[at]), static_cast<int32_t>(v[at + 1])),
-                               make_float2(rs, rs));
-        const float2 p1 = mul2(make_float2(static_cast<int32_t>(v[at + 2]), static_cast<int32_t>(v[at + 3])),
-                               make_float2(rs, rs));
-        const float2 r0 = fma2(p0, make_float2(cs.x, cs.y), make_float2(cb.x, cb.y));
-        const float2 r1 = fma2(p1, make_float2(cs.z, cs.w), make_float2(cb.z, cb.w));
-        o[j] = r0.x, o[j + 1] = r0.y, o[j + 2] = r1.x, o[j + 3] = r1.y;
-      }
-      uint32_t w[8];
-      if (a.out_fp32) {
-        float* p = static_cast<float*>(a.out) + row * a.ldo + col + 16 * q;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(o[8 * h + j]);
-          st_global_32(p + 8 * h, w);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
-        st_global_32(static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + col + 16 * q, w);
-      }
+    for (int j = 0; j < 16; j += 4) {
+      const float4 cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col + 16 * q + j));
+      float4 cb = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.bias) cb = __ldg(reinterpret_cast<const float4*>(a.bias + col + 16 * q + j));
+      const int at = 16 * q + j;
+      const float2 p0 = mul2(make_float2(static_cast<int32_t>(v[at]), static_cast<int32_t>(v[at + 1])),
+                             make_float2(rs, rs));
+      const float2 p1 = mul2(make_float2(static_cast<int32_t>(v[at + 2]), static_cast<int32_t>(v[at + 3])),
+                             make_float2(rs, rs));
+      const float2 r0 = fma2(p0, make_float2(cs.x, cs.y), make_float2(cb.x, cb.y));
+      const float2 r1 = fma2(p1, make_float2(cs.z, cs.w), make_float2(cb.z, cb.w));
+      o[j] = r0.x, o[j + 1] = r0.y, o[j + 2] = r1.x, o[j + 3] = r1.y;
     }
-    return;
-  }
+    uint32_t w[8];
+    if (a.out_fp32) {
+      float* p = static_cast<float*>(a.out) + row * a.ldo + col + 16 * q;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    if (col + j < a.N) {
-      const float cb = a.bias ? __ldg(a.bias + col + j) : 0.f;
-      const float o = fmaf(static_cast<float>(static_cast<int32_t>(v[j])) * rs,
-                           __ldg(a.w_scale + col + j), cb);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(o[8 * h + j]);
+        st_global_32(p + 8 * h, w);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16x2(o[2 * j], o[2 * j + 1]);
+      st_global_32(static_cast<__nv_bfloat16*>(a.out) + row * a.ldo + col + 16 * q, w);
+    }
+  }
+}
+
+// A warp's block of 32 rows (lane: row row0 + lane, its 32 sums in v) and
+// columns col .. col + 31 where rows start anywhere or the block is cut off:
+// through shared memory, so that a row is written by neighbouring lanes.
+__device__ __forceinline__ void finish_block(const LinearInt8Args& a, int64_t row0, int col,
+                                             float rs, const uint32_t (&v)[32], int32_t* stage) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = static_cast<int32_t>(v[j]);
+  __syncwarp();
+  const bool in = col + lane < a.N;
+  const float cs = in ? __ldg(a.w_scale + col + lane) : 0.f;
+  const float cb = in && a.bias ? __ldg(a.bias + col + lane) : 0.f;
+  const int rows = static_cast<int>(a.M - row0 < 32 ? a.M - row0 : 32);
+  for (int i = 0; i < rows; ++i) {
+    const float s = __shfl_sync(0xffffffffu, rs, i);
+    const float o = fmaf(static_cast<float>(stage[i * 33 + lane]) * s, cs, cb);
+    const int64_t at = (row0 + i) * a.ldo + col + lane;
+    if (in) {
       if (a.out_fp32)
-        static_cast<float*>(a.out)[row * a.ldo + col + j] = o;
+        static_cast<float*>(a.out)[at] = o;
       else
-        static_cast<__nv_bfloat16*>(a.out)[row * a.ldo + col + j] = __float2bfloat16_rn(o);
+        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
     }
   }
+  __syncwarp();
 }
 
 template <int kN>
@@ -355,6 +434,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp < 8) {
     // warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31, a half of the columns each
     const int quad = warp & 3, side = warp >> 2;
+    int32_t* stage = reinterpret_cast<int32_t*>(sm + S::kOffStaging) + warp * 32 * 33;
     int it = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++it) {
       const int buf = it & 1;
@@ -372,8 +452,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t v[32];
         BSA_TMEM_LD_32(src + c0, v);
         tmem_wait_ld();
-        if (row_ok) finish32(a, row, c * kN + c0, rs, v, wide);
-        __syncwarp();
+        const int col = c * kN + c0;
+        if (wide && col + 32 <= a.N) {
+          if (row_ok) finish_row(a, row, col, rs, v);
+          __syncwarp();
+        } else if (col < a.N) {
+          finish_block(a, row - lane, col, rs, v, stage);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -390,13 +475,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
-// Channels a tile: 256 unless 128 leave fewer SMs idle in the last wave.
-int linear_pair_cols(int M, int N, int K) {
-  auto waves = [&](int n) {
-    const int64_t tiles = static_cast<int64_t>((M + kPairRows - 1) / kPairRows) * ((N + n - 1) / n);
-    return (tiles + 73) / 74 * n;
-  };
-  return waves(256) <= waves(128) ? 256 : 128;
+// Channels a tile.  128 halve the work of a tile but not its A operand, so they
+// pay only where all tiles run at once (256 x 7,168 x 7,168: 21.2 us against
+// 26.0 with 256; 512 rows, in two waves: 38.0 against 28.7; 2,048: 126 and 88).
+int linear_pair_cols(int M, int N) {
+  const int64_t tiles = static_cast<int64_t>((M + kPairRows - 1) / kPairRows) * ((N + 127) / 128);
+  return tiles <= 74 ? 128 : 256;
 }
 
 template <int kN>
@@ -421,37 +505,24 @@ cudaError_t go_pair(const LinearInt8Args& a, const CUtensorMap& ma, const CUtens
   return cudaGetLastError();
 }
 
-template <int kCols, bool kSwap>
-cudaError_t go(const LinearInt8Args& a, const CUtensorMap& mr, const CUtensorMap& mc,
-               cudaStream_t st) {
-  using S = LinearSmem<kCols>;
-  auto* kernel = linear_int8_kernel<kCols, kSwap>;
-  static std::atomic<bool> done[64];
-  cudaError_t e = once_per_device(done, [&] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  });
-  if (e != cudaSuccess) return e;
-  const int rows = kSwap ? a.N : a.M, cols = kSwap ? a.M : a.N;
-  const int rt = (rows + kRowTile - 1) / kRowTile, ct = (cols + kCols - 1) / kCols;
-  const int64_t tiles = static_cast<int64_t>(rt) * ct;
-  const int grid = tiles < 148 ? static_cast<int>(tiles) : 148;
-  kernel<<<grid, kThreads, S::kBytes, st>>>(mr, mc, a, rt, ct);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
+// Few tokens: 64 x 7,168 x 7,168 take 17.8 us with the channels on the M side and 20.6 us as a pair's
+// tile; 128 take 30.8 and 21.2.
+constexpr int kFewTokens = 64;
+
 // Rows of the tensor maps' boxes (both 128 bytes wide): tokens and weights.
-void linear_int8_boxes(int M, int N, int K, int* box_a, int* box_w) {
-  *box_a = M <= 16 ? 16 : (M <= 64 ? 64 : 128);
-  *box_w = M <= 64 ? 128 : (linear_pair_cols(M, N, K) / 2);
+void linear_int8_boxes(int M, int N, int* box_a, int* box_w) {
+  *box_a = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  *box_w = M <= kFewTokens ? 128 : linear_pair_cols(M, N) / 2;
 }
 
 cudaError_t launch_linear_int8(const LinearInt8Args& a, const CUtensorMap& ma,
                                const CUtensorMap& mw, cudaStream_t st) {
-  if (a.M <= 16) return go<16, true>(a, mw, ma, st);
-  if (a.M <= 64) return go<64, true>(a, mw, ma, st);
-  return linear_pair_cols(a.M, a.N, a.K) == 256 ? go_pair<256>(a, ma, mw, st)
+  if (a.M <= 16) return go_few<16>(a, mw, ma, st);
+  if (a.M <= 32) return go_few<32>(a, mw, ma, st);
+  if (a.M <= kFewTokens) return go_few<64>(a, mw, ma, st);
+  return linear_pair_cols(a.M, a.N) == 256 ? go_pair<256>(a, ma, mw, st)
                                                 : go_pair<128>(a, ma, mw, st);
 }
 
