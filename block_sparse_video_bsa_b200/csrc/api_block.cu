@@ -245,21 +245,34 @@ int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs
   a.x_b = p->x_b, a.x_n = p->x_n, a.y_b = p->y_b, a.y_n = p->y_n, a.h_b = p->h_b, a.h_n = p->h_n;
   a.z_b = p->z_b, a.z_n = p->z_n, a.gate_b = p->gate_b, a.gate_n = p->gate_n;
   a.scale_b = p->scale_b, a.scale_n = p->scale_n, a.shift_b = p->shift_b, a.shift_n = p->shift_n;
-  // 16-byte words where every row of every operand starts on one (8 codes make 8 bytes)
-  bool vec = p->C % 8 == 0;
-  auto rows16 = [&](const void* base, int size, int64_t sb, int64_t sn) {
-    if (base) vec = vec && aligned(base, 8 * size < 16 ? 8 * size : 16) && sb % 8 == 0 && sn % 8 == 0;
+  // How the rows lie: aligned (1) where every row of every operand starts on
+  // 16 bytes (8 codes: 8 bytes); shifted (2) where the rows of x, y, h, z and of
+  // per-token vectors are all off by the same number of values; else singles (0).
+  bool vec = p->C % 8 == 0, same = true;
+  auto row = [&](const void* base, int size, int64_t sb, int64_t sn) {
+    if (!base) return;
+    const bool start = aligned(base, 8 * size < 16 ? 8 * size : 16);
+    vec = vec && start && sb % 8 == 0 && sn % 8 == 0;
+    same = same && start && (sb - p->x_b) % 8 == 0 && (sn - p->x_n) % 8 == 0;
   };
-  rows16(in->x, sx, p->x_b, p->x_n);
-  rows16(in->y, sy, p->y_b, p->y_n);
-  rows16(h, sx, p->h_b, p->h_n);
-  rows16(z, sz, p->z_b, p->z_n);
-  rows16(in->gate, sm, p->gate_b, p->gate_n);
-  rows16(in->scale, sm, p->scale_b, p->scale_n);
-  rows16(in->shift, sm, p->shift_b, p->shift_n);
+  auto vector = [&](const void* base, int size, int64_t sb, int64_t sn) {
+    if (base && sn != 0) return row(base, size, sb, sn);
+    if (base) vec = vec && aligned(base, 16) && sb % 8 == 0;
+  };
+  row(in->x, sx, p->x_b, p->x_n);
+  row(in->y, sy, p->y_b, p->y_n);
+  row(h, sx, p->h_b, p->h_n);
+  if (p->z_dtype != BSA_DTYPE_INT8)
+    row(z, sz, p->z_b, p->z_n);
+  else if (z)                       // codes are written one by one where they are not aligned
+    vec = vec && aligned(z, 8) && p->z_b % 8 == 0 && p->z_n % 8 == 0;
+  vector(in->gate, sm, p->gate_b, p->gate_n);
+  vector(in->scale, sm, p->scale_b, p->scale_n);
+  vector(in->shift, sm, p->shift_b, p->shift_n);
   for (const float* w : {in->post_weight, in->post_bias, in->pre_weight, in->pre_bias})
-    rows16(w, 4, 0, 0);
-  return cuda_status(bsa::launch_gate_norm(a, p->x_dtype == BSA_DTYPE_FP32, vec,
+    vector(w, 4, 0, 0);
+  const int mode = vec ? 1 : (same && p->C + 7 <= kMaxRow ? 2 : 0);   // the shift takes room for 7
+  return cuda_status(bsa::launch_gate_norm(a, p->x_dtype == BSA_DTYPE_FP32, mode,
                                            static_cast<cudaStream_t>(stream)));
 }
 

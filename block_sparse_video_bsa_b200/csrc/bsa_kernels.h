@@ -207,7 +207,8 @@ struct GateNormArgs {
   int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;
   int* dev_status;
 };
-cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, bool vec, cudaStream_t st);
+// mode: how the rows lie (kSingles, kAligned, kShifted of rows.cuh: 0, 1, 2).
+cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, int mode, cudaStream_t st);
 
 // Row quantisation (quant_int8.cu): B x N rows of S segments of L values.
 struct QuantInt8Args {

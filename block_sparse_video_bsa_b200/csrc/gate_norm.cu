@@ -18,9 +18,14 @@
 // depend on registers and one group's reductions hide behind another's work.
 // gate_norm_kernel for the rest: one CTA a row, the row in registers between
 // its sums, the vectors from L1 / L2.
+#include <type_traits>
+
 #include "bsa_kernels.h"
 #include "rows.cuh"
 
+#ifndef RINGK
+#define RINGK 4
+#endif
 namespace bsa {
 
 namespace {
@@ -28,11 +33,11 @@ namespace {
 // ------------------------------------------------------------ one CTA a row
 
 // v = norm(v) * weight + bias, in registers
-template <int CH, bool kVec>
+template <int CH, int kMode>
 __device__ __forceinline__ void norm_row(RowGroup& g, float (&v)[CH][8], int n, int kind, float eps,
                                          const float* weight, const float* bias) {
   if (kind == kNormLayer) {
-    const float2 mv = row_moments<CH, kVec>(g, v, n);
+    const float2 mv = row_moments<CH, kMode>(g, v, n);
     const float rs = rsqrtf(mv.y + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -44,7 +49,7 @@ __device__ __forceinline__ void norm_row(RowGroup& g, float (&v)[CH][8], int n, 
     for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int j = 0; j < 8; ++j) q = fmaf(v[c][j], v[c][j], q);   // 0 past n
-    const float rs = rsqrtf(row_sum(g, q) / n + eps);
+    const float rs = rsqrtf(row_sum(g, q) * (1.f / n) + eps);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -54,7 +59,7 @@ __device__ __forceinline__ void norm_row(RowGroup& g, float (&v)[CH][8], int n, 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float w[8];
-      load_shared8<kVec>(g, weight, n, c, w);
+      load_shared8<kMode>(g, weight, n, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] *= w[j];
     }
@@ -63,90 +68,100 @@ __device__ __forceinline__ void norm_row(RowGroup& g, float (&v)[CH][8], int n, 
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       float w[8];
-      load_shared8<kVec>(g, bias, n, c, w);
+      load_shared8<kMode>(g, bias, n, c, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] += w[j];
     }
   }
 }
 
-template <bool kVec>
+// A chunk of gate, scale or shift: one vector a token lies as the rows do.
+template <int kMode>
 __device__ __forceinline__ void load_mod8(const RowGroup& g, const void* p, int fp32, int64_t off,
-                                          int n, int c, float v[8]) {
-  if (fp32)
-    load_shared8<kVec>(g, static_cast<const float*>(p) + off, n, c, v);
-  else
-    load_shared8<kVec>(g, static_cast<const __nv_bfloat16*>(p) + off, n, c, v);
+                                          bool token, int n, int c, float v[8]) {
+  const float* f = static_cast<const float*>(p) + off;
+  const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(p) + off;
+  if (kMode == kShifted && token && row_whole<kMode>(g, c, n)) {
+    if (fp32)
+      chunk_words(f + row_index<kMode>(g, c, 0), v);
+    else
+      chunk_words(h + row_index<kMode>(g, c, 0), v);
+  } else if (fp32) {
+    load_shared8<kMode>(g, f, n, c, v);
+  } else {
+    load_shared8<kMode>(g, h, n, c, v);
+  }
 }
 
-template <bool kVec>
+template <int kMode>
 __device__ __forceinline__ void store_z8(const RowGroup& g, const GateNormArgs& a, int64_t o, int c,
                                          const float v[8]) {
   if (a.z_type == kTypeBf16)
-    store8<kVec>(g, static_cast<__nv_bfloat16*>(a.z) + o, a.C, c, v);
+    store8<kMode>(g, static_cast<__nv_bfloat16*>(a.z) + o, a.C, c, v);
   else if (a.z_type == kTypeFp32)
-    store8<kVec>(g, static_cast<float*>(a.z) + o, a.C, c, v);
+    store8<kMode>(g, static_cast<float*>(a.z) + o, a.C, c, v);
 }
 
-template <class Tx, int CH, int kThreads, int kBlocks, bool kVec>
+template <class Tx, int CH, int kThreads, int kBlocks, int kMode>
 __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const GateNormArgs a) {
   __shared__ RowReduce red;
-  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int64_t b = row / a.N, t = row - b * a.N;
+    const int64_t b = a.B == 1 ? 0 : row / a.N, t = row - b * a.N;
+    if (kMode == kShifted) g.shift = static_cast<int>((b * a.x_b + t * a.x_n) & 7);
     float h[CH][8];
-    load_row<CH, kVec>(g, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, a.C, h);
+    load_row<CH, kMode>(g, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, a.C, h);
     if (a.y) {
       float y[CH][8];
       const int64_t o = b * a.y_b + t * a.y_n;
       if (a.y_fp32)
-        load_row<CH, kVec>(g, static_cast<const float*>(a.y) + o, a.C, y);
+        load_row<CH, kMode>(g, static_cast<const float*>(a.y) + o, a.C, y);
       else
-        load_row<CH, kVec>(g, static_cast<const __nv_bfloat16*>(a.y) + o, a.C, y);
-      norm_row<CH, kVec>(g, y, a.C, a.post, a.eps, a.post_weight, a.post_bias);
+        load_row<CH, kMode>(g, static_cast<const __nv_bfloat16*>(a.y) + o, a.C, y);
+      norm_row<CH, kMode>(g, y, a.C, a.post, a.eps, a.post_weight, a.post_bias);
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         if (a.gate) {
           float m[8];
-          load_mod8<kVec>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.C, c, m);
+          load_mod8<kMode>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.gate_n != 0, a.C, c, m);
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[c][j] *= m[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           h[c][j] = fmaf(y[c][j], a.branch_scale, h[c][j] * a.residual_scale);
-          if (row_index<kVec>(g, c, j) >= a.C) h[c][j] = 0.f;   // a norm reached past the row
+          if (!row_in<kMode>(g, c, j, a.C)) h[c][j] = 0.f;   // a norm reached past the row
         }
-        if (a.h) store8<kVec>(g, static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n, a.C, c, h[c]);
+        if (a.h) store8<kMode>(g, static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n, a.C, c, h[c]);
       }
     }
     if (!a.z) continue;
-    norm_row<CH, kVec>(g, h, a.C, a.pre, a.eps, a.pre_weight, a.pre_bias);
+    norm_row<CH, kMode>(g, h, a.C, a.pre, a.eps, a.pre_weight, a.pre_bias);
     const int64_t o = b * a.z_b + t * a.z_n;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if (a.mscale) {
         float m[8];
-        load_mod8<kVec>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.C, c, m);
+        load_mod8<kMode>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.scale_n != 0, a.C, c, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], m[j], h[c][j]);
       }
       if (a.shift) {
         float m[8];
-        load_mod8<kVec>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.C, c, m);
+        load_mod8<kMode>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.shift_n != 0, a.C, c, m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] += m[j];
       }
-      store_z8<kVec>(g, a, o, c, h[c]);
+      store_z8<kMode>(g, a, o, c, h[c]);
     }
     if (a.z_type == kTypeInt8) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (row_index<kVec>(g, c, j) >= a.C) h[c][j] = 0.f;   // a layer norm's mean reached past the row
-      const float s = store_codes<CH, kVec>(g, h, a.C, static_cast<int8_t*>(a.z) + o);
+          if (!row_in<kMode>(g, c, j, a.C)) h[c][j] = 0.f;   // a layer norm's mean reached past the row
+      const float s = store_codes<CH, kMode>(g, h, a.C, static_cast<int8_t*>(a.z) + o);
       if (g.tid == 0) a.z_scale[row] = s;
     }
   }
@@ -154,9 +169,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const Gate
 
 // ------------------------------------------------------------ rows through a ring
 
-constexpr int kRingThreads = 704;      // 21 warps of rows at most, and the producer warp
-constexpr int kMaxGroups = 15;         // named barriers
-constexpr int kMaxStages = 16;
+#ifndef RT
+#define RT 704
+#endif
+constexpr int kRingThreads = RT;      // 21 warps of rows at most, and the producer warp
+constexpr int kMaxGroups = 15;         // named barriers; groups of one warp need none
+constexpr int kMaxStages = 24;
 constexpr uint32_t kRingSmem = 227 * 1024;
 
 struct RingCtl {
@@ -167,9 +185,11 @@ struct RingCtl {
 // What shared memory holds, in floats and bytes.
 struct RingShape {
   int threads, groups, stages;   // threads of a group
+  int rows, log_rows;            // rows a stage: one copy brings them where they are contiguous
   int has_gain, has_post_bias;   // gate * post_weight, gate * post_bias
   int has_a, has_b;              // pre_weight (1 + scale), pre_bias (1 + scale) + shift
   uint32_t x_bytes, y_bytes;     // of a row
+  uint32_t stage_bytes, y_at;    // of a stage; where its rows of y start
   uint32_t off_stage, off_red, off_ctl, bytes;
 };
 
@@ -187,6 +207,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 struct Oct {
   float2 p[4];
 };
+// max(|a|, |b|, m), NaN if one of them is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float m) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(m));
+  return d;
+}
 __device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ void smem8(const __nv_bfloat16* p, Oct& v) {
@@ -227,10 +253,12 @@ __device__ __forceinline__ void put8(float* p, const Oct& v) {
 }
 
 // (m, r) with norm(v) = v r + m for a row that `get` gives chunk by chunk;
-// in[c]: the chunk lies inside the row (the others are copies of its last).
+// in[c]: the chunk lies inside the row (the others are copies of its last);
+// cnt: values of the row that the warp holds, and its reciprocal (0 for none).
 template <int CH, class Get>
 __device__ __forceinline__ float2 row_affine(RowGroup& g, int n, int kind, float eps,
-                                             const bool (&in)[CH], Get get) {
+                                             const bool (&in)[CH], float cnt, float inv_cnt,
+                                             Get get) {
   if (kind == kNormNone) return make_float2(0.f, 1.f);
   if (kind == kNormRms) {
     float q = 0.f;
@@ -243,24 +271,18 @@ __device__ __forceinline__ float2 row_affine(RowGroup& g, int n, int kind, float
       for (int j = 1; j < 4; ++j) s = fma2(v.p[j], v.p[j], s);
       q += in[c] ? s.x + s.y : 0.f;
     }
-    return make_float2(0.f, rsqrtf(row_sum(g, q) / n + eps));
+    return make_float2(0.f, rsqrtf(row_sum(g, q) * (1.f / n) + eps));
   }
   // as row_moments (rows.cuh)
-  float s = 0.f, cnt = 0.f;
+  float s = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     Oct v;
     get(c, v);
     const float2 t = add2(add2(v.p[0], v.p[1]), add2(v.p[2], v.p[3]));
     s += in[c] ? t.x + t.y : 0.f;
-    cnt += in[c] ? 8.f : 0.f;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-  }
-  const float mean = cnt > 0.f ? s / cnt : 0.f;
+  const float mean = warp_sum(s) * inv_cnt;
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -275,9 +297,7 @@ __device__ __forceinline__ float2 row_affine(RowGroup& g, int n, int kind, float
     }
     q += in[c] ? t.x + t.y : 0.f;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-  const float2 mv = combine_moments(g, mean, q, cnt, n);
+  const float2 mv = combine_moments(g, mean, warp_sum(q), cnt, n);
   const float r = rsqrtf(mv.y + eps);
   return make_float2(-mv.x * r, r);
 }
@@ -298,50 +318,97 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
   if (threadIdx.x == 0) {
     for (int i = 0; i < s.stages; ++i) {
       mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], s.threads);
+      mbar_init(&ctl->empty[i], s.rows * s.threads);
     }
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
-  auto mod = [&](const void* p, int64_t off, int i) {
-    return a.mod_fp32 ? __ldg(static_cast<const float*>(p) + off + i)
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[off + i]);
-  };
-  for (int i = threadIdx.x; i < C; i += blockDim.x) {
-    const float gt = a.gate ? mod(a.gate, b * a.gate_b, i) : 1.f;
-    const float sc = a.mscale ? 1.f + mod(a.mscale, b * a.scale_b, i) : 1.f;
-    const float sh = a.shift ? mod(a.shift, b * a.shift_b, i) : 0.f;
-    const int at = folded_at(i);
-    if (s.has_gain) gain[at] = a.branch_scale * gt * (a.post_weight ? __ldg(a.post_weight + i) : 1.f);
-    if (s.has_post_bias) pbias[at] = a.branch_scale * gt * __ldg(a.post_bias + i);
-    if (s.has_a) va[at] = sc * (a.pre_weight ? __ldg(a.pre_weight + i) : 1.f);
-    if (s.has_b) vb[at] = fmaf(a.pre_bias ? __ldg(a.pre_bias + i) : 0.f, sc, sh);
-  }
   __syncthreads();
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
-  const uint32_t stage_bytes = s.x_bytes + s.y_bytes;
-  const int64_t step = gridDim.x;
+  // the CTA's rows in turn: s.rows neighbours of every gridDim.x-th block of them
+  const int blocks = (a.N + s.rows - 1) / s.rows;
 
   if (static_cast<int>(threadIdx.x) >= rows_threads) {
     if (static_cast<int>(threadIdx.x) == rows_threads) {
-      int64_t i = 0;
-      for (int64_t t = blockIdx.x; t < a.N; t += step, ++i) {
-        const int st = static_cast<int>(i % s.stages);
-        if (i >= s.stages && !mbar_wait(&ctl->empty[st], ((i / s.stages) - 1) & 1, wc)) break;
-        uint8_t* dst = sm + s.off_stage + st * stage_bytes;
-        mbar_arrive_expect_tx(&ctl->full[st], stage_bytes);
-        bulk_load(dst, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, s.x_bytes,
+      uint32_t st = 0, round = 0;
+      for (int q = blockIdx.x; q < blocks; q += gridDim.x) {
+        if (round > 0 && !mbar_wait(&ctl->empty[st], (round - 1) & 1, wc)) break;
+        const int64_t t = static_cast<int64_t>(q) * s.rows;
+        const uint32_t n = static_cast<uint32_t>(a.N - t < s.rows ? a.N - t : s.rows);
+        uint8_t* dst = sm + s.off_stage + st * s.stage_bytes;
+        mbar_arrive_expect_tx(&ctl->full[st], n * (s.x_bytes + s.y_bytes));
+        bulk_load(dst, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, n * s.x_bytes,
                   &ctl->full[st]);
         if (s.y_bytes)
-          bulk_load(dst + s.x_bytes, static_cast<const Ty*>(a.y) + b * a.y_b + t * a.y_n, s.y_bytes,
-                    &ctl->full[st]);
+          bulk_load(dst + s.y_at, static_cast<const Ty*>(a.y) + b * a.y_b + t * a.y_n,
+                    n * s.y_bytes, &ctl->full[st]);
+        if (++st == static_cast<uint32_t>(s.stages)) st = 0, ++round;
       }
       // every issued load has landed before the CTA exits
-      for (int64_t k = (i > s.stages ? i - s.stages : 0); k < i; ++k)
-        mbar_wait(&ctl->full[k % s.stages], (k / s.stages) & 1, wc);
+      for (int i = 0; i < s.stages; ++i) {
+        if (round == 0 && st == 0) break;
+        if (st == 0) st = s.stages, --round;
+        --st;
+        mbar_wait(&ctl->full[st], round & 1, wc);
+      }
     }
     return;
   }
+
+  {
+    // the vectors, 8 values a thread
+    auto mod = [&](const void* p, int64_t off, int i, float none, float v[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = none;
+      if (!p) return;
+      if (a.mod_fp32)
+        chunk_words(static_cast<const float*>(p) + off + i, v);
+      else
+        chunk_words(static_cast<const __nv_bfloat16*>(p) + off + i, v);
+    };
+    auto put = [&](float* p, int i, const float v[8]) {
+      float4* q = reinterpret_cast<float4*>(p + folded_at(i));
+      q[0] = make_float4(v[0], v[1], v[2], v[3]);
+      q[32] = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    for (int i = 8 * threadIdx.x; i < C; i += 8 * rows_threads) {
+      float gt[8], sc[8], sh[8], w[8], o[8];
+      mod(a.gate, b * a.gate_b, i, 1.f, gt);
+      mod(a.mscale, b * a.scale_b, i, 0.f, sc);
+      mod(a.shift, b * a.shift_b, i, 0.f, sh);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gt[j] *= a.branch_scale, sc[j] += 1.f, w[j] = 1.f;
+      if (s.has_gain) {
+        if (a.post_weight) chunk_words(a.post_weight + i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = gt[j] * w[j];
+        put(gain, i, o);
+      }
+      if (s.has_post_bias) {
+        chunk_words(a.post_bias + i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = gt[j] * w[j];
+        put(pbias, i, o);
+      }
+      if (s.has_a) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.f;
+        if (a.pre_weight) chunk_words(a.pre_weight + i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = sc[j] * w[j];
+        put(va, i, o);
+      }
+      if (s.has_b) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 0.f;
+        if (a.pre_bias) chunk_words(a.pre_bias + i, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = fmaf(w[j], sc[j], sh[j]);
+        put(vb, i, o);
+      }
+    }
+  }
+  asm volatile("bar.sync 0, %0;" ::"r"(rows_threads) : "memory");   // the producer is on its way
 
   const int group = threadIdx.x / s.threads;
   RowGroup g{static_cast<int>(threadIdx.x) - group * s.threads, s.threads, 1 + group,
@@ -351,19 +418,37 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
   bool in[CH];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int k = row_index<true>(g, c, 0);
+    const int k = row_index<kAligned>(g, c, 0);
     in[c] = k < C;
     at[c] = in[c] ? k : C - 8;
   }
-  uint32_t st = group % s.stages, round = group / s.stages;
-  for (int64_t t = blockIdx.x + group * step; t < a.N; t += s.groups * step) {
+  float cnt = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) cnt += in[c] ? 8.f : 0.f;
+  cnt = warp_sum(cnt);
+  const float inv_cnt = cnt > 0.f ? 1.f / cnt : 0.f;
+  // row `sub` of the CTA's stage number `seq`, stage seq % stages
+  uint32_t sub = group % s.rows, st = group / s.rows, round = 0;
+  int q = blockIdx.x + st * gridDim.x;
+  while (st >= static_cast<uint32_t>(s.stages)) st -= s.stages, ++round;
+  for (;;) {
+    if (q >= blocks) break;
+    const int64_t t = static_cast<int64_t>(q) * s.rows + sub;
     // the whole group goes on or none of it
     if (!g.all(mbar_wait(&ctl->full[st], round & 1, wc))) break;
-    const Tx* xs = reinterpret_cast<const Tx*>(sm + s.off_stage + st * stage_bytes);
-    const Ty* ys = reinterpret_cast<const Ty*>(sm + s.off_stage + st * stage_bytes + s.x_bytes);
+    const uint8_t* stage = sm + s.off_stage + st * s.stage_bytes;
+    uint64_t* empty = &ctl->empty[st];
+    const Tx* xs = reinterpret_cast<const Tx*>(stage + sub * s.x_bytes);
+    const Ty* ys = reinterpret_cast<const Ty*>(stage + s.y_at + sub * s.y_bytes);
+    sub += s.groups;
+    const uint32_t on = sub >> s.log_rows;
+    sub &= s.rows - 1;
+    q += on * gridDim.x;
+    for (st += on; st >= static_cast<uint32_t>(s.stages); st -= s.stages) ++round;
+    if (t >= a.N) continue;             // past the last stage's rows
     Oct h[CH];
     if (s.y_bytes) {
-      const float2 mr = row_affine<CH>(g, C, a.post, a.eps, in,
+      const float2 mr = row_affine<CH>(g, C, a.post, a.eps, in, cnt, inv_cnt,
                                        [&](int c, Oct& v) { smem8(ys + at[c], v); });
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
@@ -396,7 +481,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(x.p[j], pair(a.residual_scale), h[c].p[j]);
       }
-      mbar_arrive(&ctl->empty[st]);
+      mbar_arrive(empty);
       if (a.h) {
         Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
 #pragma unroll
@@ -406,13 +491,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c) smem8(xs + at[c], h[c]);
-      mbar_arrive(&ctl->empty[st]);
+      mbar_arrive(empty);
     }
-    st += s.groups;
-    while (st >= static_cast<uint32_t>(s.stages)) st -= s.stages, ++round;
     if (!a.z) continue;
     const float2 mr =
-        row_affine<CH>(g, C, a.pre, a.eps, in, [&](int c, Oct& v) { v = h[c]; });
+        row_affine<CH>(g, C, a.pre, a.eps, in, cnt, inv_cnt, [&](int c, Oct& v) { v = h[c]; });
 #pragma unroll
     for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -445,13 +528,33 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
       for (int c = 0; c < CH; ++c)
         if (in[c]) put8(static_cast<float*>(a.z) + o + at[c], h[c]);
     } else {
-      float x[CH][8];
+      float m = 0.f;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
+      for (int c = 0; c < CH; ++c) {
+        // a copy of the row's last chunk does not change its maximum
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[c][j] = in[c] ? (j & 1 ? h[c].p[j >> 1].y : h[c].p[j >> 1].x) : 0.f;
-      const float sc = store_codes<CH, true>(g, x, C, static_cast<int8_t*>(a.z) + o);
+        for (int j = 0; j < 4; ++j) m = max3_abs_nan(h[c].p[j].x, h[c].p[j].y, m);
+      }
+      m = row_max_abs(g, m);
+      const bool finite = m <= 3.402823466e38f;
+      m = finite ? fmaxf(m, kInt8Floor) : m;
+      const float inv = __fdiv_rn(127.f, m);
+      int8_t* zo = static_cast<int8_t*>(a.z) + o;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          // the codes of rows.cuh (code_bits), two at a time
+          const float2 u = add2(mul2(h[c].p[2 * k], pair(inv)), pair(12582912.f));
+          const float2 v = add2(mul2(h[c].p[2 * k + 1], pair(inv)), pair(12582912.f));
+          const uint32_t lo = __byte_perm(__float_as_uint(u.x), __float_as_uint(u.y), 0x0040);
+          const uint32_t hi = __byte_perm(__float_as_uint(v.x), __float_as_uint(v.y), 0x0040);
+          w[k] = finite ? __byte_perm(lo, hi, 0x5410) : 0u;
+        }
+        if (in[c]) *reinterpret_cast<uint2*>(zo + at[c]) = make_uint2(w[0], w[1]);
+      }
+      const float sc = finite ? __fdiv_rn(m, 127.f) : __uint_as_float(0x7fc00000u);
       if (g.tid == 0) a.z_scale[b * a.N + t] = sc;
     }
   }
@@ -466,16 +569,19 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   const int per = 148 / a.B > 0 ? 148 / a.B : 1;
   s->x_bytes = static_cast<uint32_t>(a.C) * (x_fp32 ? 4 : 2);
   s->y_bytes = a.y ? static_cast<uint32_t>(a.C) * (a.y_fp32 ? 4 : 2) : 0;
-  if (s->x_bytes + s->y_bytes < 4096) return false;
   const int vecs = a.C / 8;
-  *ch = 4;
-  s->threads = ((vecs + 3) / 4 + 31) / 32 * 32;
+  *ch = vecs <= 32 ? 1 : (vecs <= 64 ? 2 : 4);
+  s->threads = ((vecs + *ch - 1) / *ch + 31) / 32 * 32;
   if (s->threads > kRingThreads - 32) return false;
   s->groups = (kRingThreads - 32) / s->threads;
-  if (s->groups > kMaxGroups) s->groups = kMaxGroups;
-  // at least four rows a group, or filling the vectors does not pay: 2,000 rows of 1,024 take
-  // 12.3 us here and 8.3 us with a CTA a row
-  if (a.N < 4 * per * s->groups || a.B > 65535) return false;
+  if (s->threads > 32 && s->groups > kMaxGroups) s->groups = kMaxGroups;
+  if (a.N < RINGK * per * s->groups || a.B > 65535) return false;
+  // short rows: 8 KB a stage and one copy for it, where they lie one after another
+  s->rows = 1, s->log_rows = 0;
+  if (a.x_n == a.C && (!a.y || a.y_n == a.C))
+    while (s->rows < 16 && s->rows * (s->x_bytes + s->y_bytes) < 8192)
+      s->rows *= 2, ++s->log_rows;
+  if (s->rows * (s->x_bytes + s->y_bytes) < 4096) return false;
   s->has_gain = a.y && (a.gate || a.post_weight || a.branch_scale != 1.f);
   s->has_post_bias = a.y && a.post_bias;
   s->has_a = a.z && (a.mscale || a.pre_weight);
@@ -484,7 +590,9 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
       (s->has_gain + s->has_post_bias + s->has_a + s->has_b) * ((a.C + 255) & ~255) * 4u;
   s->off_stage = (vectors + 127) & ~127u;
   const uint32_t fixed = s->groups * static_cast<uint32_t>(sizeof(RowReduce)) + sizeof(RingCtl) + 16;
-  const uint32_t stage = s->x_bytes + s->y_bytes;
+  const uint32_t stage = s->rows * (s->x_bytes + s->y_bytes);
+  s->stage_bytes = stage;
+  s->y_at = s->rows * s->x_bytes;
   if (s->off_stage + fixed + 2 * stage > kRingSmem) return false;
   int stages = static_cast<int>((kRingSmem - s->off_stage - fixed) / stage);
   s->stages = stages < kMaxStages ? stages : kMaxStages;
@@ -495,9 +603,9 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   return true;
 }
 
-template <class Tx, class Ty>
-cudaError_t launch_ring(const GateNormArgs& a, const RingShape& s, dim3 grid, cudaStream_t st) {
-  auto* kernel = gate_norm_ring_kernel<Tx, Ty, 4>;
+template <class Tx, class Ty, int CH>
+cudaError_t launch_ring_ch(const GateNormArgs& a, const RingShape& s, dim3 grid, cudaStream_t st) {
+  auto* kernel = gate_norm_ring_kernel<Tx, Ty, CH>;
   static std::atomic<bool> done[64];
   cudaError_t e = once_per_device(done, [&] {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
@@ -507,17 +615,25 @@ cudaError_t launch_ring(const GateNormArgs& a, const RingShape& s, dim3 grid, cu
   return cudaGetLastError();
 }
 
-template <class Tx, bool kVec>
+template <class Tx, class Ty>
+cudaError_t launch_ring(const GateNormArgs& a, const RingShape& s, int ch, dim3 grid,
+                        cudaStream_t st) {
+  if (ch == 1) return launch_ring_ch<Tx, Ty, 1>(a, s, grid, st);
+  if (ch == 2) return launch_ring_ch<Tx, Ty, 2>(a, s, grid, st);
+  return launch_ring_ch<Tx, Ty, 4>(a, s, grid, st);
+}
+
+template <class Tx, int kMode>
 cudaError_t launch(const GateNormArgs& a, int ch, int threads, int blocks, cudaStream_t st) {
   auto go = [&](auto k) {
     k<<<blocks, threads, 0, st>>>(a);
     return cudaGetLastError();
   };
-  if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, 1, kVec>);
-  if (ch == 2) return threads <= 512 ? go(gate_norm_kernel<Tx, 2, 512, 2, kVec>)
-                                     : go(gate_norm_kernel<Tx, 2, 1024, 1, kVec>);
-  return threads <= 512 ? go(gate_norm_kernel<Tx, 4, 512, 1, kVec>)
-                        : go(gate_norm_kernel<Tx, 4, 1024, 1, kVec>);
+  if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, 1, kMode>);
+  if (ch == 2) return threads <= 512 ? go(gate_norm_kernel<Tx, 2, 512, 2, kMode>)
+                                     : go(gate_norm_kernel<Tx, 2, 1024, 1, kMode>);
+  return threads <= 512 ? go(gate_norm_kernel<Tx, 4, 512, 1, kMode>)
+                        : go(gate_norm_kernel<Tx, 4, 1024, 1, kMode>);
 }
 
 }  // namespace
@@ -533,26 +649,29 @@ void row_shape(int n, int64_t rows, int* ch, int* threads) {
   *threads = ((vecs + c - 1) / c + 31) / 32 * 32;
 }
 
-cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, bool vec, cudaStream_t st) {
+cudaError_t launch_gate_norm(const GateNormArgs& a, bool x_fp32, int mode, cudaStream_t st) {
   RingShape s = {};
   int ch, threads;
   dim3 grid;
   using bf16 = __nv_bfloat16;
-  if (vec && ring_shape(a, x_fp32, &s, &ch, &grid)) {
+  if (mode == kAligned && ring_shape(a, x_fp32, &s, &ch, &grid)) {
     if (x_fp32)
-      return a.y_fp32 ? launch_ring<float, float>(a, s, grid, st)
-                      : launch_ring<float, bf16>(a, s, grid, st);
-    return a.y_fp32 ? launch_ring<bf16, float>(a, s, grid, st)
-                    : launch_ring<bf16, bf16>(a, s, grid, st);
+      return a.y_fp32 ? launch_ring<float, float>(a, s, ch, grid, st)
+                      : launch_ring<float, bf16>(a, s, ch, grid, st);
+    return a.y_fp32 ? launch_ring<bf16, float>(a, s, ch, grid, st)
+                    : launch_ring<bf16, bf16>(a, s, ch, grid, st);
   }
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
-  row_shape(a.C, rows, &ch, &threads);
+  row_shape(a.C + (mode == kShifted ? 7 : 0), rows, &ch, &threads);
   const int blocks = static_cast<int>(rows < (1 << 30) ? rows : (1 << 30));
-  if (vec)
-    return x_fp32 ? launch<float, true>(a, ch, threads, blocks, st)
-                  : launch<bf16, true>(a, ch, threads, blocks, st);
-  return x_fp32 ? launch<float, false>(a, ch, threads, blocks, st)
-                : launch<bf16, false>(a, ch, threads, blocks, st);
+  auto go = [&](auto tag) {
+    constexpr int kMode = decltype(tag)::value;
+    return x_fp32 ? launch<float, kMode>(a, ch, threads, blocks, st)
+                  : launch<bf16, kMode>(a, ch, threads, blocks, st);
+  };
+  if (mode == kAligned) return go(std::integral_constant<int, kAligned>());
+  if (mode == kShifted) return go(std::integral_constant<int, kShifted>());
+  return go(std::integral_constant<int, kSingles>());
 }
 
 }  // namespace bsa

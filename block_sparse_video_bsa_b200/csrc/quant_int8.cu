@@ -14,10 +14,10 @@ namespace bsa {
 namespace {
 
 // Any rows, fp32 in registers.
-template <class Tx, int CH, bool kVec>
+template <class Tx, int CH, int kMode>
 __global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args a) {
   __shared__ RowReduce red;
-  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   const int n = a.S * a.L;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -25,18 +25,18 @@ __global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args
     const Tx* src = static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n;
     float x[CH][8];
     if (a.S == 1) {
-      load_row<CH, kVec>(g, src, n, x);
+      load_row<CH, kMode>(g, src, n, x);
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int i = row_index<kVec>(g, c, j);
+          const int i = row_index<kMode>(g, c, j);
           const int s = i / a.L;
           x[c][j] = i < n ? to_f32(src[s * a.x_s + (i - s * a.L)]) : 0.f;
         }
     }
-    const float s = store_codes<CH, kVec>(g, x, n, a.q + row * a.q_ld);
+    const float s = store_codes<CH, kMode>(g, x, n, a.q + row * a.q_ld);
     if (g.tid == 0) a.scale[row] = s;
   }
 }
@@ -47,13 +47,13 @@ __global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args
 template <int CH, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(const QuantInt8Args a) {
   __shared__ RowReduce red;
-  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0};
+  RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   const int n = a.S * a.L;
   int64_t off[CH];                               // of this thread's chunks in every row
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int i = row_index<true>(g, c, 0);
+    const int i = row_index<kAligned>(g, c, 0);
     const int s = a.S == 1 ? 0 : i / a.L;        // a chunk lies in one segment
     off[c] = s * a.x_s + (i - s * a.L);
   }
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(cons
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       w[c] = make_uint4(0, 0, 0, 0);
-      if (row_index<true>(g, c, 0) < n) w[c] = ld_stream_v4(src + off[c]);
+      if (row_index<kAligned>(g, c, 0) < n) w[c] = ld_stream_v4(src + off[c]);
     }
     uint32_t m = 0;
 #pragma unroll
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(cons
     int8_t* q = a.q + row * a.q_ld;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int i = row_index<true>(g, c, 0);
+      const int i = row_index<kAligned>(g, c, 0);
       float x[8];
       bf16x8_to_f32(w[c], x);
       uint2 k = make_uint2(0, 0);
@@ -91,15 +91,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(cons
   }
 }
 
-template <class Tx, bool kVec>
+template <class Tx, int kMode>
 cudaError_t launch(const QuantInt8Args& a, int ch, int threads, int blocks, cudaStream_t st) {
   auto go = [&](auto k) {
     k<<<blocks, threads, 0, st>>>(a);
     return cudaGetLastError();
   };
-  if (ch == 1) return go(quant_int8_kernel<Tx, 1, kVec>);
-  if (ch == 2) return go(quant_int8_kernel<Tx, 2, kVec>);
-  return go(quant_int8_kernel<Tx, 4, kVec>);
+  if (ch == 1) return go(quant_int8_kernel<Tx, 1, kMode>);
+  if (ch == 2) return go(quant_int8_kernel<Tx, 2, kMode>);
+  return go(quant_int8_kernel<Tx, 4, kMode>);
 }
 
 }  // namespace
@@ -128,10 +128,10 @@ cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cud
     return go(quant_int8_bf16_kernel<4, 1024, 1>);
   }
   if (vec)
-    return x_fp32 ? launch<float, true>(a, ch, threads, blocks, st)
-                  : launch<__nv_bfloat16, true>(a, ch, threads, blocks, st);
-  return x_fp32 ? launch<float, false>(a, ch, threads, blocks, st)
-                : launch<__nv_bfloat16, false>(a, ch, threads, blocks, st);
+    return x_fp32 ? launch<float, kAligned>(a, ch, threads, blocks, st)
+                  : launch<__nv_bfloat16, kAligned>(a, ch, threads, blocks, st);
+  return x_fp32 ? launch<float, kSingles>(a, ch, threads, blocks, st)
+                : launch<__nv_bfloat16, kSingles>(a, ch, threads, blocks, st);
 }
 
 }  // namespace bsa

@@ -1,12 +1,17 @@
 // One row of up to 32,768 values spread over a CTA or a group of its warps: loads, stores, the row's
 // sums and the int8 codes of a row (gate_norm.cu, quant_int8.cu).
 //
-// A thread holds CH chunks of 8 values in registers.  kVec: chunk c of thread
-// t is the 8 neighbours at (c * threads + t) * 8, read and written as 16-byte
-// words; else value j of chunk c sits at (c * 8 + j) * threads + t, so that
-// scalar accesses of rows that do not start on 16 bytes are still contiguous
-// across a warp.  Everything done to a row is per value or a sum over all of
-// it, so the arrangement does not matter to it.
+// A thread holds CH chunks of 8 values in registers; kMode says which:
+//   kAligned  chunk c of thread t is the 8 neighbours at (c threads + t) 8, read
+//             and written as 16-byte words (every row starts on one);
+//   kShifted  the same moved back by `shift` values, so that the chunks start on
+//             16-byte boundaries of rows that do not: rows of an odd length one
+//             after another, all operands off by the same amount.  The one or
+//             two chunks that a row's ends cut go value by value;
+//   kSingles  value j of chunk c sits at (c 8 + j) threads + t: scalar accesses,
+//             still contiguous across a warp.
+// Everything done to a row is per value or a sum over all of it, so the
+// arrangement does not matter to it.
 #pragma once
 
 #include "bsa_device.cuh"
@@ -32,12 +37,14 @@ struct RowGroup {
   int bar;             // named barrier of the group
   RowReduce* red;
   int turn;            // slot of the next reduction
+  int shift;           // values before the row that its first chunk starts at (kShifted)
   __device__ __forceinline__ int warps() const { return threads >> 5; }
   __device__ __forceinline__ void sync() const {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
   }
   // True on every thread when it is true on all (one barrier).
   __device__ __forceinline__ bool all(bool ok) const {
+    if (threads == 32) return __all_sync(0xffffffffu, ok);
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -51,9 +58,24 @@ struct RowGroup {
   }
 };
 
-template <bool kVec>
+enum { kSingles = 0, kAligned = 1, kShifted = 2 };
+
+template <int kMode>
 __device__ __forceinline__ int row_index(const RowGroup& g, int c, int j) {
-  return kVec ? (c * g.threads + g.tid) * 8 + j : (c * 8 + j) * g.threads + g.tid;
+  if (kMode == kSingles) return (c * 8 + j) * g.threads + g.tid;
+  return (c * g.threads + g.tid) * 8 + j - (kMode == kShifted ? g.shift : 0);
+}
+template <int kMode>
+__device__ __forceinline__ bool row_in(const RowGroup& g, int c, int j, int n) {
+  const int i = row_index<kMode>(g, c, j);
+  return kMode == kShifted ? static_cast<unsigned>(i) < static_cast<unsigned>(n) : i < n;
+}
+// Chunk c lies inside the row and starts on a 16-byte boundary.
+template <int kMode>
+__device__ __forceinline__ bool row_whole(const RowGroup& g, int c, int n) {
+  if (kMode == kSingles) return false;
+  const int i = row_index<kMode>(g, c, 0);
+  return kMode == kAligned ? i < n : (i >= 0 && i + 8 <= n);
 }
 
 __device__ __forceinline__ uint4 ld_row_v4(const void* p) {
@@ -67,56 +89,38 @@ __device__ __forceinline__ uint4 ld_row_v4(const void* p) {
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 
-// x[c][j] = p[...] (0 past n).  A row is read once: it skips L1.
-template <int CH, bool kVec>
-__device__ __forceinline__ void load_row(const RowGroup& g, const __nv_bfloat16* p, int n, float (&x)[CH][8]) {
-  if constexpr (kVec) {
-    uint4 w[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int i = row_index<true>(g, c, 0);
-      w[c] = make_uint4(0, 0, 0, 0);
-      if (i < n) w[c] = ld_row_v4(p + i);
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) bf16x8_to_f32(w[c], x[c]);
-  } else {
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(g, c, j);
-        x[c][j] = i < n ? to_f32(p[i]) : 0.f;
-      }
-  }
+// Values as loaded: a chunk is one (bf16) or two (fp32) 16-byte words.
+__device__ __forceinline__ void chunk_words(const __nv_bfloat16* p, float x[8]) {
+  bf16x8_to_f32(ld_row_v4(p), x);
 }
-template <int CH, bool kVec>
-__device__ __forceinline__ void load_row(const RowGroup& g, const float* p, int n, float (&x)[CH][8]) {
+__device__ __forceinline__ void chunk_words(const float* p, float x[8]) {
+  const uint4 a = ld_row_v4(p), b = ld_row_v4(p + 4);
+  x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y), x[2] = __uint_as_float(a.z);
+  x[3] = __uint_as_float(a.w), x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
+  x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+}
+
+// x[c][j] = the row's value, 0 outside it.  A row is read once: it skips L1.
+template <int CH, int kMode, class T>
+__device__ __forceinline__ void load_row(const RowGroup& g, const T* p, int n, float (&x)[CH][8]) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    if constexpr (kVec) {
-      const int i = row_index<true>(g, c, 0);
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (i < n) a = ld_row_v4(p + i), b = ld_row_v4(p + i + 4);
-      x[c][0] = __uint_as_float(a.x), x[c][1] = __uint_as_float(a.y);
-      x[c][2] = __uint_as_float(a.z), x[c][3] = __uint_as_float(a.w);
-      x[c][4] = __uint_as_float(b.x), x[c][5] = __uint_as_float(b.y);
-      x[c][6] = __uint_as_float(b.z), x[c][7] = __uint_as_float(b.w);
+    if (row_whole<kMode>(g, c, n)) {
+      chunk_words(p + row_index<kMode>(g, c, 0), x[c]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(g, c, j);
-        x[c][j] = i < n ? p[i] : 0.f;
-      }
+      for (int j = 0; j < 8; ++j)
+        x[c][j] = kMode != kAligned && row_in<kMode>(g, c, j, n) ? to_f32(p[row_index<kMode>(g, c, j)]) : 0.f;
     }
   }
 }
 
-// One chunk of a vector that many rows share (kept in L1).
-template <bool kVec>
+// One chunk of a vector that many rows share (kept in L1); it starts on 16
+// bytes itself, so that only kAligned chunks do.
+template <int kMode>
 __device__ __forceinline__ void load_shared8(const RowGroup& g, const float* p, int n, int c, float v[8]) {
-  if constexpr (kVec) {
-    const int i = row_index<true>(g, c, 0);
+  if (kMode == kAligned) {
+    const int i = row_index<kMode>(g, c, 0);
     float4 a = make_float4(0, 0, 0, 0), b = a;
     if (i < n) {
       a = __ldg(reinterpret_cast<const float4*>(p + i));
@@ -125,86 +129,78 @@ __device__ __forceinline__ void load_shared8(const RowGroup& g, const float* p, 
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(g, c, j);
-      v[j] = i < n ? __ldg(p + i) : 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+      v[j] = row_in<kMode>(g, c, j, n) ? __ldg(p + row_index<kMode>(g, c, j)) : 0.f;
   }
 }
-template <bool kVec>
-__device__ __forceinline__ void load_shared8(const RowGroup& g, const __nv_bfloat16* p, int n, int c, float v[8]) {
-  if constexpr (kVec) {
-    const int i = row_index<true>(g, c, 0);
+template <int kMode>
+__device__ __forceinline__ void load_shared8(const RowGroup& g, const __nv_bfloat16* p, int n, int c,
+                                             float v[8]) {
+  if (kMode == kAligned) {
+    const int i = row_index<kMode>(g, c, 0);
     uint4 w = make_uint4(0, 0, 0, 0);
     if (i < n) w = __ldg(reinterpret_cast<const uint4*>(p + i));
     bf16x8_to_f32(w, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(g, c, j);
-      v[j] = i < n ? __bfloat162float(p[i]) : 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+      v[j] = row_in<kMode>(g, c, j, n) ? to_f32(p[row_index<kMode>(g, c, j)]) : 0.f;
   }
 }
 
 // One chunk of a row, rounded once to the stored type (to nearest even).
-template <bool kVec>
-__device__ __forceinline__ void store8(const RowGroup& g, __nv_bfloat16* p, int n, int c, const float v[8]) {
-  if constexpr (kVec) {
-    const int i = row_index<true>(g, c, 0);
-    if (i < n)
-      *reinterpret_cast<uint4*>(p + i) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                    pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  } else {
+__device__ __forceinline__ void put_chunk(__nv_bfloat16* p, const float v[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void put_chunk(float* p, const float v[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void put_value(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put_value(float* p, float v) { *p = v; }
+template <int kMode, class T>
+__device__ __forceinline__ void store8(const RowGroup& g, T* p, int n, int c, const float v[8]) {
+  if (row_whole<kMode>(g, c, n)) {
+    put_chunk(p + row_index<kMode>(g, c, 0), v);
+  } else if (kMode != kAligned) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(g, c, j);
-      if (i < n) p[i] = __float2bfloat16_rn(v[j]);
-    }
+    for (int j = 0; j < 8; ++j)
+      if (row_in<kMode>(g, c, j, n)) put_value(p + row_index<kMode>(g, c, j), v[j]);
   }
 }
-template <bool kVec>
-__device__ __forceinline__ void store8(const RowGroup& g, float* p, int n, int c, const float v[8]) {
-  if constexpr (kVec) {
-    const int i = row_index<true>(g, c, 0);
-    if (i < n) {
-      reinterpret_cast<float4*>(p + i)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p + i)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
+
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = row_index<false>(g, c, j);
-      if (i < n) p[i] = v[j];
-    }
-  }
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// This lane's share of what every warp of the row left in the current slot
+// (warp w's in lane w), after the barrier.
+__device__ __forceinline__ float4 row_partials(RowGroup& g, float4 mine) {
+  const int lane = g.tid & 31;
+  if (lane == 0) g.red->part[g.turn][g.tid >> 5] = mine;
+  g.sync();
+  const float4 p = lane < g.warps() ? g.red->part[g.turn][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+  g.turn ^= 1;
+  return p;
 }
 
 // Sum over the row's threads.
 __device__ __forceinline__ float row_sum(RowGroup& g, float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warps = g.warps();
-  if (warps == 1) return v;
-  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5].x = v;
-  g.sync();
-  v = 0.f;
-  for (int w = 0; w < warps; ++w) v += g.red->part[g.turn][w].x;
-  g.turn ^= 1;
-  return v;
+  v = warp_sum(v);
+  if (g.warps() == 1) return v;
+  return warp_sum(row_partials(g, make_float4(v, 0.f, 0.f, 0.f)).x);
 }
 
 // Largest value over the row's threads; v >= 0 or NaN, and a NaN anywhere wins (as an
 // unsigned word it is above every number).
 __device__ __forceinline__ float row_max_abs(RowGroup& g, float v) {
   uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
-  const int warps = g.warps();
-  if (warps == 1) return __uint_as_float(m);
-  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5].x = __uint_as_float(m);
-  g.sync();
-  m = 0;
-  for (int w = 0; w < warps; ++w) m = max(m, __float_as_uint(g.red->part[g.turn][w].x));
-  g.turn ^= 1;
+  if (g.warps() > 1)
+    m = __reduce_max_sync(0xffffffffu, __float_as_uint(
+                              row_partials(g, make_float4(__uint_as_float(m), 0.f, 0.f, 0.f)).x));
   return __uint_as_float(m);
 }
 
@@ -212,61 +208,44 @@ __device__ __forceinline__ float row_max_abs(RowGroup& g, float v) {
 // mean, sum of squares about it and count (exact identity, one barrier).
 __device__ __forceinline__ float2 combine_moments(RowGroup& g, float mean, float q, float cnt,
                                                   int n) {
-  const int warps = g.warps();
-  if (warps == 1) return make_float2(mean, q / n);
-  if ((g.tid & 31) == 0) g.red->part[g.turn][g.tid >> 5] = make_float4(mean, q, cnt, 0.f);
-  g.sync();
-  float total = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    const float4 p = g.red->part[g.turn][w];
-    total = fmaf(p.x, p.z, total);
-  }
-  const float all = total / n;
-  float m2 = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    const float4 p = g.red->part[g.turn][w];
-    m2 += fmaf((p.x - all) * (p.x - all), p.z, p.y);
-  }
-  g.turn ^= 1;
-  return make_float2(all, m2 / n);
+  const float inv = 1.f / n;
+  if (g.warps() == 1) return make_float2(mean, q * inv);
+  const float4 p = row_partials(g, make_float4(mean, q, cnt, 0.f));
+  const float all = warp_sum(p.x * p.z) * inv;
+  const float d = p.x - all;
+  return make_float2(all, warp_sum(fmaf(d * d, p.z, p.y)) * inv);
 }
 
 // Mean and mean squared deviation of the row's n values.  Each warp takes the
 // mean of its own values and the squares about it, and the warps' results are
 // combined exactly (sum of squares + counts x squared distance of the means):
 // no difference of large sums, and one barrier.
-template <int CH, bool kVec>
+template <int CH, int kMode>
 __device__ __forceinline__ float2 row_moments(RowGroup& g, const float (&x)[CH][8], int n) {
   float s = 0.f, cnt = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s += x[c][j];          // 0 past n
-    if constexpr (kVec) {
-      cnt += row_index<true>(g, c, 0) < n ? 8.f : 0.f;
+    for (int j = 0; j < 8; ++j) s += x[c][j];          // 0 outside the row
+    if (kMode == kAligned) {
+      cnt += row_whole<kMode>(g, c, n) ? 8.f : 0.f;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cnt += row_index<false>(g, c, j) < n ? 1.f : 0.f;
+      for (int j = 0; j < 8; ++j) cnt += row_in<kMode>(g, c, j, n) ? 1.f : 0.f;
     }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-  }
+  s = warp_sum(s), cnt = warp_sum(cnt);
   const float mean = cnt > 0.f ? s / cnt : 0.f;
   float q = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const bool in = row_index<kVec>(g, c, j) < n;
+      const bool in = row_in<kMode>(g, c, j, n);
       const float d = x[c][j] - mean;
       q = in ? fmaf(d, d, q) : q;
     }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-  return combine_moments(g, mean, q, cnt, n);
+  return combine_moments(g, mean, warp_sum(q), cnt, n);
 }
 
 // Code of one value, in the low byte: the product is rounded to fp32, and the
@@ -285,14 +264,14 @@ __device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
 // factors rounded to fp32, |code| <= 127.  A row that holds a NaN or an
 // infinity has a scale that is not finite (NaN) and codes 0: its products are
 // NaN.  Stores 8 (or single) codes; returns the scale to every thread.
-template <int CH, bool kVec>
+template <int CH, int kMode>
 __device__ __forceinline__ float store_codes(RowGroup& g, const float (&x)[CH][8], int n, int8_t* q) {
   float m = 0.f;
 #pragma unroll
   for (int c = 0; c < CH; ++c)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t a = __float_as_uint(x[c][j]) & 0x7fffffffu;   // 0 past n
+      const uint32_t a = __float_as_uint(x[c][j]) & 0x7fffffffu;   // 0 outside the row
       m = __uint_as_float(max(__float_as_uint(m), a));
     }
   m = row_max_abs(g, m);
@@ -301,17 +280,16 @@ __device__ __forceinline__ float store_codes(RowGroup& g, const float (&x)[CH][8
   const float inv = __fdiv_rn(127.f, m);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    if constexpr (kVec) {
-      const int i = row_index<true>(g, c, 0);
+    if (kMode == kAligned) {
       uint2 w = make_uint2(0, 0);
       if (finite) w = make_uint2(codes4(x[c], inv), codes4(x[c] + 4, inv));
-      if (i < n) *reinterpret_cast<uint2*>(q + i) = w;
+      if (row_whole<kMode>(g, c, n))
+        *reinterpret_cast<uint2*>(q + row_index<kMode>(g, c, 0)) = w;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = row_index<false>(g, c, j);
-        if (i < n) q[i] = finite ? static_cast<int8_t>(code_bits(x[c][j], inv)) : 0;
-      }
+      for (int j = 0; j < 8; ++j)
+        if (row_in<kMode>(g, c, j, n))
+          q[row_index<kMode>(g, c, j)] = finite ? static_cast<int8_t>(code_bits(x[c][j], inv)) : 0;
     }
   }
   return finite ? __fdiv_rn(m, 127.f) : __uint_as_float(0x7fc00000u);
