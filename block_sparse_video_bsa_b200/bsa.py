@@ -90,6 +90,22 @@ class bsa_linear_int8_params(ctypes.Structure):
                 + [(n, _i64) for n in ("lda", "ldw", "ldo")] + [("dev_status", ctypes.c_void_p)])
 
 
+class bsa_block_params(ctypes.Structure):
+    _fields_ = ([(n, _i32) for n in ("C", "x_dtype", "mod_dtype", "pre", "post")]
+                + [(n, _f32) for n in ("eps", "residual_scale", "branch_scale", "qk_eps",
+                                       "rope_scale")]
+                + [(n, _i32) for n in ("rotary_dim", "layout", "axes")]
+                + [("axis_pairs", _i32 * 4)]
+                + [(n, _i64) for n in ("gate_b", "gate_n", "scale_b", "scale_n", "shift_b",
+                                       "shift_n", "pos_b", "pos_n", "ld_qkv", "ld_out")])
+
+
+class bsa_block_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "gate", "scale", "shift", "pre_weight", "pre_bias", "post_weight", "post_bias", "w_qkv",
+        "s_qkv", "b_qkv", "w_out", "s_out", "b_out", "q_weight", "k_weight", "positions", "freqs")]
+
+
 _lib = None
 _P = ctypes.POINTER(bsa_params)
 _F8 = ctypes.POINTER(bsa_fp8_operands)
@@ -153,6 +169,10 @@ _SIGS["bsa_gate_norm"] = (ctypes.c_int, [ctypes.POINTER(bsa_gate_norm_params),
                                          ctypes.POINTER(bsa_gate_norm_inputs)] + [_vp] * 4)
 _SIGS["bsa_quantize_int8"] = (ctypes.c_int, [ctypes.POINTER(bsa_quantize_int8_params)] + [_vp] * 4)
 _SIGS["bsa_linear_int8"] = (ctypes.c_int, [ctypes.POINTER(bsa_linear_int8_params)] + [_vp] * 7)
+_BP = ctypes.POINTER(bsa_block_params)
+_SIGS["bsa_forward_block_workspace_bytes"] = (ctypes.c_size_t, [_P, _BP])
+_SIGS["bsa_forward_block"] = (ctypes.c_int, [_P, _BP, ctypes.POINTER(bsa_block_weights)]
+                              + [_vp] * 3 + [ctypes.c_size_t, _vp])
 BSA_MAX_EXTRA_TOKENS = 512
 
 
@@ -574,6 +594,17 @@ def _raw_stream(device):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+# torch.empty's argument handling costs a microsecond more than empty_strided's
+_new = torch.empty_strided
+
+
+def _packed(shape):
+    """Strides of a contiguous tensor."""
+    strides, n = [], 1
+    for d in reversed(shape):
+        strides.append(n)
+        n *= max(d, 1)
+    return tuple(reversed(strides))
 
 
 def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_length=0,
@@ -627,7 +658,7 @@ def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inver
         if y is None:
             y = (out_dtype or dtype, shape, (H * N * 128, N * 128, 128, 1), device)
         _need(y[0] in _FLOATS and y[1] == shape and y[2][3] == 1, where)
-        want.append((y[1], y[0]))
+        want.append((tuple(y[1]), _packed(y[1]), y[0]))
         kinds.setdefault((H, stride, dtype, y[2], y[0]), []).append(i)
     launches = []
     for (H, stride, dtype, ostride, odtype), ids in kinds.items():
@@ -656,8 +687,8 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
         with _elsewhere(device, stream, "rotary"):
             return rotary(q, k, v, positions, freqs, layout, axis_pairs, q_weight, k_weight, eps,
                           scale, inverse, out, out_dtype)
-    outs = [w if w is None else (y if y is not None else
-                                 torch.empty(w[0], dtype=w[1], device=freqs.device))
+    where = freqs.device
+    outs = [y if w is None or y is not None else _new(w[0], w[1], dtype=w[2], device=where)
             for w, y in zip(want, outs)]
     qkv, weights, st = (q, k, v), (q_weight, k_weight, None), _raw_stream(device)
     for p, ids in launches:
@@ -709,7 +740,7 @@ def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, re
         DTYPES[mods[0]] if mods else 1, 2 if quantize and want_z else DTYPES[z_dtype], eps,
         residual_scale, branch_scale, *_rows(x, C), *_rows(y, C), *h, N * ld, ld,
         *_mod(gate, B, N, C, where), *_mod(scale, B, N, C, where), *_mod(shift, B, N, C, where))
-    return device, ctypes.byref(p), x[1], B * N, C, ld
+    return device, ctypes.byref(p), ((B, N, C), (N * C, C, 1)), ((B * N, ld), (ld, 1)), C, ld
 
 
 def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weight=None,
@@ -722,7 +753,7 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     x, y [B, N, C]; gate, scale, shift [C], [B, C], [B, 1, C] or [B, N, C]; weights and biases fp32
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
-    device, p, shape, rows, C, ld = _gate_norm_plan(
+    device, p, shape, codes, C, ld = _gate_norm_plan(
         _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
         (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out), pre,
         post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z)
@@ -733,12 +764,12 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
                              want_z)
     h, z, zs = h_out, None, None
     if h is None and y is not None:
-        h = torch.empty(shape, dtype=x.dtype, device=x.device)
+        h = _new(*shape, dtype=x.dtype, device=x.device)
     if want_z and quantize:
-        z = torch.empty((rows, ld), dtype=torch.int8, device=x.device)
-        zs = torch.empty(rows, dtype=torch.float32, device=x.device)
+        z = _new(*codes, dtype=torch.int8, device=x.device)
+        zs = _new(codes[0][:1], (1,), dtype=torch.float32, device=x.device)
     elif want_z:
-        z = torch.empty(shape, dtype=z_dtype, device=x.device)
+        z = _new(*shape, dtype=z_dtype, device=x.device)
     i = bsa_gate_norm_inputs(x.data_ptr(), _addr(y), _addr(gate), _addr(scale), _addr(shift),
                              _addr(post_weight), _addr(post_bias), _addr(pre_weight),
                              _addr(pre_bias))
@@ -775,8 +806,8 @@ def quantize_int8(x, stream=None):
     if not _here(device, stream):
         with _elsewhere(device, stream, "quantize_int8"):
             return quantize_int8(x)
-    codes = torch.empty((rows, ld), dtype=torch.int8, device=x.device)
-    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    codes = _new((rows, ld), (ld, 1), dtype=torch.int8, device=x.device)
+    scale = _new((rows,), (1,), dtype=torch.float32, device=x.device)
     _check(lib().bsa_quantize_int8(p, x.data_ptr(), codes.data_ptr(), scale.data_ptr(),
                                    _raw_stream(device)), "bsa_quantize_int8")
     return (codes if ld == K else codes[:, :K]), scale
@@ -809,11 +840,83 @@ def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out
     if not _here(device, stream):
         with _elsewhere(device, stream, "linear_int8"):
             return linear_int8(a, a_scale, w, w_scale, bias, out_dtype, out, dev_status)
-    o = out if out is not None else torch.empty(p[:2], dtype=out_dtype, device=a.device)
+    o = out
+    if o is None:
+        o = _new(p[:2], (p[1], 1), dtype=out_dtype, device=a.device)
     _check(lib().bsa_linear_int8(ctypes.byref(bsa_linear_int8_params(*p, _addr(dev_status))),
                                  a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
                                  _addr(bias), o.data_ptr(), _raw_stream(device)), "bsa_linear_int8")
     return o
+
+
+def forward_block(x, w_qkv, s_qkv, w_out, s_out, positions, freqs, top_k, gate=None, scale=None,
+                  shift=None, b_qkv=None, b_out=None, pre="rms", pre_weight=None, pre_bias=None,
+                  post="none", post_weight=None, post_bias=None, q_weight=None, k_weight=None,
+                  layout="half", axis_pairs=None, rope_scale=1.0, eps=1e-6, qk_eps=1e-6,
+                  residual_scale=1.0, branch_scale=1.0, prefix=0, variant="anchor", out=None,
+                  ws=None, dev_status=None, stream=None):
+    """bsa_forward_block: the attention half of a block on token rows x [B, N, C] (contiguous).
+
+    w_qkv [3 H 128, C] and w_out [C, H 128] are int8 codes with one scale a row, as
+    ``quantize_int8`` makes them; the vectors are those of ``gate_norm`` and ``rotary``.  ``out`` may
+    be x.  Returns out."""
+    where = "forward_block"
+    vectors = (pre_weight, pre_bias, post_weight, post_bias)
+    sigs = [_sig(t) for t in (w_qkv, s_qkv, w_out, s_out, positions, freqs, gate, scale, shift,
+                              b_qkv, b_out, *vectors, q_weight, k_weight, out, ws, dev_status)]
+    device = _one_device(where, _sig(x), *sigs)
+    _need(x.dim() == 3 and x.dtype in _FLOATS and x.is_contiguous(), where)
+    B, N, C = x.shape
+    for w in (w_qkv, w_out):
+        _need(w.dim() == 2 and w.dtype == torch.int8 and w.stride(1) == 1, where)
+    H = w_out.shape[1] // 128
+    _need(H >= 1 and w_qkv.shape == (3 * H * 128, C) and w_out.shape == (C, H * 128), where)
+    for t, n in ((s_qkv, 3 * H * 128), (s_out, C)):
+        _need(t is not None, where)
+        _vector(_sig(t), n, where)
+    for t, n in ((b_qkv, 3 * H * 128), (b_out, C), *((v, C) for v in vectors), (q_weight, 128),
+                 (k_weight, 128)):
+        _vector(_sig(t), n, where)
+    pairs = [freqs.numel()] if axis_pairs is None else list(axis_pairs)
+    _need(freqs.dtype == torch.float64 and freqs.is_contiguous() and freqs.dim() == 1
+          and 1 <= len(pairs) <= 4 and sum(pairs) == freqs.numel(), where)
+    pos = positions[:, None] if positions.dim() == 1 else positions
+    _need(pos.dtype == torch.int32 and pos.dim() in (2, 3) and pos.shape[-2:] == (N, len(pairs))
+          and (len(pairs) == 1 or pos.stride(-1) == 1)
+          and (pos.dim() == 2 or pos.shape[0] in (1, B)), where)
+    mods = [t.dtype for t in (gate, scale, shift) if t is not None]
+    _need(all(d in _FLOATS and d == mods[0] for d in mods), where)
+    _need(pre in NORMS and post in NORMS, where)
+    _need(out is None or (out.shape == x.shape and out.dtype == x.dtype and out.is_contiguous()),
+          where)
+    if not _here(device, stream):
+        with _elsewhere(device, stream, where):
+            return forward_block(x, w_qkv, s_qkv, w_out, s_out, positions, freqs, top_k, gate,
+                                 scale, shift, b_qkv, b_out, pre, pre_weight, pre_bias, post,
+                                 post_weight, post_bias, q_weight, k_weight, layout, axis_pairs,
+                                 rope_scale, eps, qk_eps, residual_scale, branch_scale, prefix,
+                                 variant, out, ws, dev_status)
+    p = params(B, H, N, top_k, prefix, variant, dev_status=dev_status)
+    bp = bsa_block_params(
+        C, DTYPES[x.dtype], DTYPES[mods[0]] if mods else 1, NORMS[pre], NORMS[post], eps,
+        residual_scale, branch_scale, qk_eps, rope_scale, 2 * freqs.numel(), ROPE_LAYOUTS[layout],
+        len(pairs), (_i32 * 4)(*pairs), *_mod(_sig(gate), B, N, C, where),
+        *_mod(_sig(scale), B, N, C, where), *_mod(_sig(shift), B, N, C, where),
+        pos.stride(0) if pos.dim() == 3 and pos.shape[0] > 1 else 0, pos.stride(-2),
+        w_qkv.stride(0), w_out.stride(0))
+    bw = bsa_block_weights(*[_addr(t) for t in (gate, scale, shift, *vectors, w_qkv, s_qkv, b_qkv,
+                                                w_out, s_out, b_out, q_weight, k_weight, pos,
+                                                freqs)])
+    if ws is None:
+        n = lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp))
+        _need(n > 0, where)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    _check(lib().bsa_forward_block(ctypes.byref(p), ctypes.byref(bp), ctypes.byref(bw), _addr(x),
+                                   _addr(out), _addr(ws), ws.numel() * ws.element_size(),
+                                   _raw_stream(device)), "bsa_forward_block")
+    return out
 
 
 # --------------------------------------------------------------- allocation helpers

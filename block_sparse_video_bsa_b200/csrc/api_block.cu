@@ -57,48 +57,14 @@ bool disjoint(int64_t row, int64_t na, int64_t sa, int64_t nb, int64_t sb, int64
   return true;
 }
 
-}  // namespace
-
-extern "C" {
+// Each entry checks its arguments and, with `launch`, enqueues its kernel: a
+// path of several calls checks all of them before the first launch.
 
 // ------------------------------------------------------------------ rotary
 
-int bsa_rotary_freqs(int32_t pairs, double base, int32_t scaling, double factor,
-                     double trained_length, double fast_turns, double slow_turns, double* freqs,
-                     float* scale) {
-  if (pairs < 0 || pairs > 64 || (pairs > 0 && !freqs) || !scale) return BSA_ERR_INVALID;
-  if (!(base > 1.0) || !std::isfinite(base)) return BSA_ERR_INVALID;
-  if (scaling < BSA_ROPE_PLAIN || scaling > BSA_ROPE_BY_PARTS) return BSA_ERR_INVALID;
-  const bool by_parts = scaling == BSA_ROPE_YARN || scaling == BSA_ROPE_BY_PARTS;
-  if (scaling != BSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
-    return BSA_ERR_INVALID;
-  if (by_parts && (!(trained_length >= 1.0) || !std::isfinite(trained_length) ||
-                   !(fast_turns > slow_turns) || !(slow_turns >= 0.0) ||
-                   !std::isfinite(fast_turns)))
-    return BSA_ERR_INVALID;
-  const double two_pi = 6.283185307179586476925286766559;
-  if (scaling == BSA_ROPE_NTK && pairs > 1)
-    base *= std::pow(factor, static_cast<double>(pairs) / (pairs - 1));
-  for (int i = 0; i < pairs; ++i) {
-    double f = std::pow(base, -static_cast<double>(i) / pairs);
-    if (scaling == BSA_ROPE_LINEAR) f /= factor;
-    if (by_parts) {
-      // share of the pair's own frequency: 1 from fast_turns over the trained
-      // length on, 0 up to slow_turns
-      const double turns = trained_length * f / two_pi;
-      double keep = (turns - slow_turns) / (fast_turns - slow_turns);
-      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
-      f = f * keep + f / factor * (1.0 - keep);
-    }
-    freqs[i] = f;
-  }
-  *scale = scaling == BSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
-  return BSA_OK;
-}
-
-int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, const void* v,
+int rotary_entry(const bsa_rotary_params* params, const void* q, const void* k, const void* v,
                const int32_t* positions, const double* freqs, const float* q_weight,
-               const float* k_weight, void* Q, void* K, void* V, void* stream) {
+               const float* k_weight, void* Q, void* K, void* V, void* stream, bool launch) {
   if (!params) return BSA_ERR_INVALID;
   bsa_rotary_params own = *params;
   bsa_rotary_params* p = &own;
@@ -165,6 +131,7 @@ int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, co
   for (int64_t s : {p->out_b, p->out_h, p->out_n})
     if (s * so % 16) return BSA_ERR_ALIGN;
   if ((positions && !aligned(positions, 4)) || (freqs && !aligned(freqs, 8))) return BSA_ERR_ALIGN;
+  if (!launch) return BSA_OK;
   int rc = check_device();
   if (rc) return rc;
   a.B = p->B, a.H = p->H, a.N = p->N, a.r = p->rotary_dim;
@@ -184,8 +151,8 @@ int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, co
 
 // ------------------------------------------------------------------ gate norm
 
-int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,
-                  float* z_scale, void* stream) {
+int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,
+                  float* z_scale, void* stream, bool launch) {
   if (!params || !in) return BSA_ERR_INVALID;
   bsa_gate_norm_params own = *params;
   bsa_gate_norm_params* p = &own;
@@ -230,6 +197,7 @@ int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs
     if (m && !aligned(m, sm)) return BSA_ERR_ALIGN;
   for (const float* w : {in->post_weight, in->post_bias, in->pre_weight, in->pre_bias})
     if (w && !aligned(w, 4)) return BSA_ERR_ALIGN;
+  if (!launch) return BSA_OK;
   int rc = check_device();
   if (rc) return rc;
   bsa::GateNormArgs a = {};
@@ -278,8 +246,8 @@ int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs
 
 // ------------------------------------------------------------------ int8
 
-int bsa_quantize_int8(const bsa_quantize_int8_params* params, const void* x, int8_t* codes, float* scale,
-                      void* stream) {
+int quantize_int8_entry(const bsa_quantize_int8_params* params, const void* x, int8_t* codes, float* scale,
+                      void* stream, bool launch) {
   if (!params) return BSA_ERR_INVALID;
   bsa_quantize_int8_params own = *params;
   bsa_quantize_int8_params* p = &own;
@@ -303,6 +271,7 @@ int bsa_quantize_int8(const bsa_quantize_int8_params* params, const void* x, int
            range_of(codes, 1, K, rows, p->ld)))
     return BSA_ERR_INVALID;
   if (!aligned(x, sx) || !aligned(scale, 4)) return BSA_ERR_ALIGN;
+  if (!launch) return BSA_OK;
   int rc = check_device();
   if (rc) return rc;
   bsa::QuantInt8Args a = {};
@@ -316,9 +285,9 @@ int bsa_quantize_int8(const bsa_quantize_int8_params* params, const void* x, int
                                             static_cast<cudaStream_t>(stream)));
 }
 
-int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const float* a_scale,
+int linear_int8_entry(const bsa_linear_int8_params* params, const int8_t* a, const float* a_scale,
                     const int8_t* w, const float* w_scale, const float* bias, void* out,
-                    void* stream) {
+                    void* stream, bool launch) {
   if (!params) return BSA_ERR_INVALID;
   bsa_linear_int8_params own = *params;
   bsa_linear_int8_params* p = &own;
@@ -338,6 +307,7 @@ int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const
   if (!aligned(a, 16) || !aligned(w, 16) || p->lda % 16 || p->ldw % 16 || !aligned(out, so) ||
       !aligned(a_scale, 4) || !aligned(w_scale, 4) || (bias && !aligned(bias, 4)))
     return BSA_ERR_ALIGN;
+  if (!launch) return BSA_OK;
   int rc = check_device();
   if (rc) return rc;
   bsa::EncodeTiledFn enc = bsa::encode_fn();
@@ -364,6 +334,202 @@ int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const
   l.out = out, l.ldo = p->ldo, l.out_fp32 = p->out_dtype == BSA_DTYPE_FP32;
   l.dev_status = p->dev_status;
   return cuda_status(bsa::launch_linear_int8(l, ma, mw, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ block path
+
+// Intermediates of the block path carved from one buffer (each piece 256-byte
+// aligned).  What follows the attention takes the place of the projection.
+struct BlockWs {
+  int8_t* z8;
+  float* zs;
+  uint8_t* qkv;                 // bf16 [B, N, 3, H, 128]
+  uint8_t *Q, *K, *V;
+  uint8_t* O;                   // over qkv
+  int8_t* o8;
+  float* os;
+  uint8_t* y;
+  uint8_t* attn;
+};
+
+size_t block_carve(const bsa_params* p, int C, uint8_t* base, BlockWs* w) {
+  const size_t rows = static_cast<size_t>(p->B) * p->N, hd = static_cast<size_t>(p->H) * 128;
+  const size_t ldc = (static_cast<size_t>(C) + 15) / 16 * 16;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* q = base ? base + off : nullptr;
+    off += bsa::round256(bytes);
+    return q;
+  };
+  BlockWs o = {};
+  o.z8 = reinterpret_cast<int8_t*>(take(rows * ldc));
+  o.zs = reinterpret_cast<float*>(take(rows * 4));
+  o.Q = take(rows * hd * 2);
+  o.K = take(rows * hd * 2);
+  o.V = take(rows * hd * 2);
+  o.attn = take(bsa_workspace_bytes(p));
+  const size_t mark = off;
+  o.qkv = take(rows * 3 * hd * 2);
+  const size_t first = off;
+  off = mark;
+  o.O = take(rows * hd * 2);
+  o.o8 = reinterpret_cast<int8_t*>(take(rows * hd));
+  o.os = reinterpret_cast<float*>(take(rows * 4));
+  o.y = take(rows * C * 2);
+  if (off < first) off = first;
+  if (w) *w = o;
+  return off;
+}
+
+// The calls of the path on one workspace; with launch = false only their checks.
+int block_run(const bsa_params* p, const bsa_block_params* bp, const bsa_block_weights* bw,
+              const void* x, void* out, const BlockWs& w, void* stream, bool launch) {
+  const int B = p->B, N = p->N, H = p->H, C = bp->C;
+  const int64_t hd = static_cast<int64_t>(H) * 128, ldc = (C + 15) / 16 * 16;
+  bsa_gate_norm_params g = {};
+  g.B = B, g.N = N, g.C = C, g.pre = bp->pre, g.post = bp->post;
+  g.x_dtype = bp->x_dtype, g.mod_dtype = bp->mod_dtype;
+  g.y_dtype = BSA_DTYPE_BF16, g.z_dtype = BSA_DTYPE_INT8;
+  g.eps = bp->eps, g.residual_scale = bp->residual_scale, g.branch_scale = bp->branch_scale;
+  g.x_b = g.y_b = g.h_b = static_cast<int64_t>(N) * C;
+  g.x_n = g.y_n = g.h_n = C;
+  g.z_b = N * ldc, g.z_n = ldc;
+  g.gate_b = bp->gate_b, g.gate_n = bp->gate_n, g.scale_b = bp->scale_b, g.scale_n = bp->scale_n;
+  g.shift_b = bp->shift_b, g.shift_n = bp->shift_n;
+  g.dev_status = p->dev_status;
+  bsa_gate_norm_inputs in = {};
+  in.x = x, in.scale = bw->scale, in.shift = bw->shift;
+  in.pre_weight = bw->pre_weight, in.pre_bias = bw->pre_bias;
+  int rc = gate_norm_entry(&g, &in, nullptr, w.z8, w.zs, stream, launch);
+  if (rc) return rc;
+
+  bsa_linear_int8_params l = {};
+  l.M = B * N, l.N = static_cast<int>(3 * hd), l.K = C, l.out_dtype = BSA_DTYPE_BF16;
+  l.lda = ldc, l.ldw = bp->ld_qkv, l.ldo = 3 * hd, l.dev_status = p->dev_status;
+  if ((rc = linear_int8_entry(&l, w.z8, w.zs, bw->w_qkv, bw->s_qkv, bw->b_qkv, w.qkv, stream,
+                              launch)))
+    return rc;
+
+  bsa_rotary_params r = {};
+  r.B = B, r.H = H, r.N = N, r.D = p->D;
+  r.rotary_dim = bp->rotary_dim, r.layout = bp->layout, r.axes = bp->axes;
+  for (int i = 0; i < 4; ++i) r.axis_pairs[i] = bp->axis_pairs[i];
+  r.in_dtype = r.out_dtype = BSA_DTYPE_BF16;
+  r.scale = bp->rope_scale, r.eps = bp->qk_eps;
+  r.in_b = N * 3 * hd, r.in_n = 3 * hd, r.in_h = 128;
+  r.out_b = N * hd, r.out_h = static_cast<int64_t>(N) * 128, r.out_n = 128;
+  r.pos_b = bp->pos_b, r.pos_n = bp->pos_n;
+  if ((rc = rotary_entry(&r, w.qkv, w.qkv + hd * 2, w.qkv + 2 * hd * 2, bw->positions, bw->freqs,
+                         bw->q_weight, bw->k_weight, w.Q, w.K, w.V, stream, launch)))
+    return rc;
+
+  if (launch && (rc = bsa_forward(p, w.Q, w.K, w.V, w.O, nullptr, w.attn, bsa_workspace_bytes(p),
+                                  stream)))
+    return rc;
+
+  bsa_quantize_int8_params q = {};
+  q.B = B, q.N = N, q.S = H, q.L = 128, q.x_dtype = BSA_DTYPE_BF16;
+  q.x_b = N * hd, q.x_n = 128, q.x_s = static_cast<int64_t>(N) * 128, q.ld = hd;
+  if ((rc = quantize_int8_entry(&q, w.O, w.o8, w.os, stream, launch))) return rc;
+
+  l.N = C, l.K = static_cast<int>(hd), l.lda = hd, l.ldw = bp->ld_out, l.ldo = C;
+  if ((rc = linear_int8_entry(&l, w.o8, w.os, bw->w_out, bw->s_out, bw->b_out, w.y, stream, launch)))
+    return rc;
+
+  in = {};
+  in.x = x, in.y = w.y, in.gate = bw->gate;
+  in.post_weight = bw->post_weight, in.post_bias = bw->post_bias;
+  g.z_dtype = BSA_DTYPE_BF16;
+  return gate_norm_entry(&g, &in, out, nullptr, nullptr, stream, launch);
+}
+
+bool block_valid(const bsa_params* p, const bsa_block_params* bp) {
+  return p && bp && bsa_workspace_bytes(p) != 0 && bp->C >= 1 && bp->C <= kMaxRow &&
+         p->H <= kMaxRow / 128 && static_cast<int64_t>(p->B) * p->N <= INT32_MAX;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bsa_rotary_freqs(int32_t pairs, double base, int32_t scaling, double factor,
+                     double trained_length, double fast_turns, double slow_turns, double* freqs,
+                     float* scale) {
+  if (pairs < 0 || pairs > 64 || (pairs > 0 && !freqs) || !scale) return BSA_ERR_INVALID;
+  if (!(base > 1.0) || !std::isfinite(base)) return BSA_ERR_INVALID;
+  if (scaling < BSA_ROPE_PLAIN || scaling > BSA_ROPE_BY_PARTS) return BSA_ERR_INVALID;
+  const bool by_parts = scaling == BSA_ROPE_YARN || scaling == BSA_ROPE_BY_PARTS;
+  if (scaling != BSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return BSA_ERR_INVALID;
+  if (by_parts && (!(trained_length >= 1.0) || !std::isfinite(trained_length) ||
+                   !(fast_turns > slow_turns) || !(slow_turns >= 0.0) ||
+                   !std::isfinite(fast_turns)))
+    return BSA_ERR_INVALID;
+  const double two_pi = 6.283185307179586476925286766559;
+  if (scaling == BSA_ROPE_NTK && pairs > 1)
+    base *= std::pow(factor, static_cast<double>(pairs) / (pairs - 1));
+  for (int i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -static_cast<double>(i) / pairs);
+    if (scaling == BSA_ROPE_LINEAR) f /= factor;
+    if (by_parts) {
+      // share of the pair's own frequency: 1 from fast_turns over the trained
+      // length on, 0 up to slow_turns
+      const double turns = trained_length * f / two_pi;
+      double keep = (turns - slow_turns) / (fast_turns - slow_turns);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    freqs[i] = f;
+  }
+  *scale = scaling == BSA_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return BSA_OK;
+}
+
+int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, const void* v,
+               const int32_t* positions, const double* freqs, const float* q_weight,
+               const float* k_weight, void* Q, void* K, void* V, void* stream) {
+  return rotary_entry(params, q, k, v, positions, freqs, q_weight, k_weight, Q, K, V, stream, true);
+}
+
+int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,
+                  float* z_scale, void* stream) {
+  return gate_norm_entry(params, in, h, z, z_scale, stream, true);
+}
+
+int bsa_quantize_int8(const bsa_quantize_int8_params* params, const void* x, int8_t* codes, float* scale,
+                      void* stream) {
+  return quantize_int8_entry(params, x, codes, scale, stream, true);
+}
+
+int bsa_linear_int8(const bsa_linear_int8_params* params, const int8_t* a, const float* a_scale,
+                    const int8_t* w, const float* w_scale, const float* bias, void* out,
+                    void* stream) {
+  return linear_int8_entry(params, a, a_scale, w, w_scale, bias, out, stream, true);
+}
+
+size_t bsa_forward_block_workspace_bytes(const bsa_params* p, const bsa_block_params* bp) {
+  return block_valid(p, bp) ? block_carve(p, bp->C, nullptr, nullptr) : 0;
+}
+
+int bsa_forward_block(const bsa_params* p, const bsa_block_params* bp, const bsa_block_weights* w,
+                      const void* x, void* out, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!block_valid(p, bp) || !w || !x || !out || !workspace) return BSA_ERR_INVALID;
+  if (workspace_bytes < block_carve(p, bp->C, nullptr, nullptr)) return BSA_ERR_INVALID;
+  if (!aligned(workspace, 256)) return BSA_ERR_ALIGN;
+  // the workspace lies apart from the rows that are read and written
+  const int64_t rows = static_cast<int64_t>(p->B) * p->N;
+  if (!float_type(bp->x_dtype)) return BSA_ERR_INVALID;
+  const int sx = type_size(bp->x_dtype);
+  const Range ws{reinterpret_cast<uintptr_t>(workspace),
+                 reinterpret_cast<uintptr_t>(workspace) + block_carve(p, bp->C, nullptr, nullptr)};
+  if (meet(ws, range_of(x, sx, bp->C, rows, bp->C)) || meet(ws, range_of(out, sx, bp->C, rows, bp->C)))
+    return BSA_ERR_INVALID;
+  BlockWs b;
+  block_carve(p, bp->C, static_cast<uint8_t*>(workspace), &b);
+  int rc = block_run(p, bp, w, x, out, b, stream, false);
+  if (rc) return rc;
+  return block_run(p, bp, w, x, out, b, stream, true);
 }
 
 }  // extern "C"

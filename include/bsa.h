@@ -648,6 +648,45 @@ int bsa_linear_int8(const bsa_linear_int8_params* p, const int8_t* a, const floa
                     const int8_t* w, const float* w_scale, const float* bias, void* out,
                     void* stream);
 
+typedef struct {
+  int32_t C;                     /* width of the hidden states, <= 32768      */
+  int32_t x_dtype, mod_dtype;    /* of x and out; of gate, scale and shift    */
+  int32_t pre, post;             /* bsa_norm                                  */
+  float eps, residual_scale, branch_scale;   /* as bsa_gate_norm_params       */
+  float qk_eps, rope_scale;      /* as bsa_rotary_params eps and scale        */
+  int32_t rotary_dim, layout, axes, axis_pairs[4];
+  int64_t gate_b, gate_n, scale_b, scale_n, shift_b, shift_n;
+  int64_t pos_b, pos_n;
+  int64_t ld_qkv, ld_out;        /* bytes from row to row of the weights      */
+} bsa_block_params;
+
+typedef struct {
+  const void *gate, *scale, *shift;
+  const float *pre_weight, *pre_bias, *post_weight, *post_bias;
+  const int8_t* w_qkv;           /* [3 H 128, C]: q, k, v in turn             */
+  const float *s_qkv, *b_qkv;    /* scales, and biases or NULL                */
+  const int8_t* w_out;           /* [C, H 128]                                */
+  const float *s_out, *b_out;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const double* freqs;
+} bsa_block_weights;
+
+/* Workspace of bsa_forward_block in bytes (0 if p or bp is invalid). */
+size_t bsa_forward_block_workspace_bytes(const bsa_params* p, const bsa_block_params* bp);
+
+/* The attention half of a block on token rows x [B, N, C], H <= 256:
+ *   z = pre(x) (1 + scale) + shift      as int8 rows        bsa_gate_norm
+ *   q, k, v = z w_qkv^T + b_qkv         bf16 [B, N, 3, H, 128]  bsa_linear_int8
+ *   Q, K, V = norm and rotary           [B, H, N, 128]      bsa_rotary
+ *   O = bsa_forward(p, Q, K, V)
+ *   y = int8(O) w_out^T + b_out         bf16                bsa_quantize_int8, bsa_linear_int8
+ *   out = residual_scale x + branch_scale gate post(y)      bsa_gate_norm
+ * in order on `stream`; each step as its own entry says.  out may be x. */
+int bsa_forward_block(const bsa_params* p, const bsa_block_params* bp, const bsa_block_weights* w,
+                      const void* x, void* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* Human-readable name of a bsa_status value (static string). */
 const char* bsa_status_string(int status);
 

@@ -250,3 +250,38 @@ def test_wrappers_refuse_tensors_that_are_not_on_a_device():
         with pytest.raises(bsa.BsaError) as e:
             call()
         assert e.value.status == bsa.BSA_ERR_INVALID
+
+
+def _block(ptr=None, ws=A + 8 * BIG, nbytes=1 << 34, x=A, out=A + BIG, p=None, **kw):
+    bp = dict(C=256, x_dtype=0, mod_dtype=1, pre=1, post=1, eps=1e-6, residual_scale=1.0, branch_scale=1.0, qk_eps=1e-6, rope_scale=1.0,
+              rotary_dim=128, layout=0, axes=1, gate_b=256, scale_b=256, shift_b=256, pos_n=1, ld_qkv=256, ld_out=256)
+    bp.update(kw)
+    s = bsa.bsa_block_params(**bp)
+    s.axis_pairs = (ctypes.c_int32 * 4)(bp["rotary_dim"] // 2)
+    w = dict(gate=A, scale=A, shift=A, w_qkv=A + 2 * BIG, s_qkv=A, w_out=A + 3 * BIG, s_out=A, positions=A, freqs=A)
+    w.update(ptr or {})
+    p = p or bsa.params(1, 2, 1000, 3)
+    return bsa.lib().bsa_forward_block(ctypes.byref(p), ctypes.byref(s), ctypes.byref(bsa.bsa_block_weights(**w)), x, out, ws, nbytes, None)
+
+
+def test_forward_block_refusals():
+    # every step's arguments are checked before the first launch
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    for kw in (dict(C=0), dict(C=32769), dict(x_dtype=2), dict(pre=5), dict(eps=-1.0), dict(rotary_dim=130), dict(qk_eps=float("nan")),
+               dict(ld_qkv=128), dict(ld_out=128), dict(nbytes=1000), dict(x=None), dict(out=None), dict(ws=None),
+               dict(ws=A), dict(ws=A + BIG - 256), dict(out=A + 256), dict(p=bsa.params(1, 257, 1000, 3)), dict(p=bsa.params(1, 2, 0, 3)),
+               dict(ptr=dict(w_qkv=None)), dict(ptr=dict(s_out=None)), dict(ptr=dict(positions=None)), dict(post=-1)):
+        assert _block(**kw) == inv, kw
+    for kw in (dict(ws=A + 8 * BIG + 16), dict(x=A + 1), dict(ptr=dict(w_out=A + 3 * BIG + 8)), dict(ptr=dict(q_weight=A + 4)),
+               dict(ptr=dict(b_out=A + 2)), dict(ld_out=260), dict(ptr=dict(post_bias=A + 1))):
+        assert _block(**kw) == al, kw
+
+
+def test_forward_block_workspace():
+    p, bp = bsa.params(1, 56, 37_740, 64), bsa.bsa_block_params(C=7168)
+    n = bsa.lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp))
+    rows = 37_740
+    want = rows * 7168 + rows * 4 + 3 * rows * 7168 * 2 + bsa.bsa_workspace_bytes(p) + rows * 3 * 7168 * 2
+    assert want <= n <= want + 8 * 256
+    bp.C = 0
+    assert bsa.lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp)) == 0

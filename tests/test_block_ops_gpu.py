@@ -477,3 +477,84 @@ def test_gate_norm_of_many_rows_in_wider_buffers(cuda_dev):
     hr, zr, eh, ez = gate_norm_bounds(x[keep][None], y[keep][None], None, None, None, "layer", "rms", [None] * 4, 1e-6, 1.0, 1.0)
     close(h[keep][None], hr, eh)
     close(z[keep][None], zr, ez)
+
+
+# ------------------------------------------------------------------ the block path
+
+def block_case(B, N, H, C, seed, dtype=torch.bfloat16):
+    r = lambda i, *s, **k: rnd(seed + i, *s, **k)  # noqa: E731
+    w_qkv, s_qkv = bsa.quantize_int8(r(0, 3 * H * 128, C, scale=C ** -0.5))
+    w_out, s_out = bsa.quantize_int8(r(1, C, H * 128, scale=(H * 128) ** -0.5))
+    pos = torch.stack((torch.arange(N) // 24, torch.arange(N) // 6 % 4, torch.arange(N) % 6), 1).to(torch.int32).cuda()
+    freqs, m = bsa.rotary_freqs([22, 21, 21])
+    return dict(x=r(2, B, N, C, dtype=dtype), w_qkv=w_qkv, s_qkv=s_qkv, w_out=w_out, s_out=s_out, positions=pos, freqs=freqs, rope_scale=m,
+                gate=r(3, B, C), scale=r(4, B, C, scale=0.3), shift=r(5, B, C, scale=0.3), b_qkv=r(6, 3 * H * 128, scale=0.1),
+                b_out=r(7, C, scale=0.1), pre="layer", post="rms", post_weight=1 + r(8, C, scale=0.1), q_weight=1 + r(9, 128, scale=0.1),
+                k_weight=1 + r(10, 128, scale=0.1), layout="interleaved", axis_pairs=[22, 21, 21])
+
+
+def by_steps(c, top_k, prefix, variant):
+    B, N, C = c["x"].shape
+    H = c["w_out"].shape[1] // 128
+    _, (a, sa) = bsa.gate_norm(c["x"], scale=c["scale"], shift=c["shift"], pre=c["pre"], quantize=True)
+    qkv = bsa.linear_int8(a, sa, c["w_qkv"], c["s_qkv"], c["b_qkv"]).view(B, N, 3, H, 128)
+    Q, K, V = bsa.rotary(*(qkv[:, :, i].transpose(1, 2) for i in range(3)), c["positions"], c["freqs"], c["layout"], c["axis_pairs"],
+                         c["q_weight"], c["k_weight"], 1e-6, c["rope_scale"])
+    O = bsa.forward(Q, K, V, top_k, prefix, variant)
+    y = bsa.linear_int8(*bsa.quantize_int8(O), c["w_out"], c["s_out"], c["b_out"]).view(B, N, C)
+    h, _ = bsa.gate_norm(c["x"], y, c["gate"], post=c["post"], post_weight=c["post_weight"], want_z=False)
+    return h
+
+
+@pytest.mark.parametrize("B,N,H,C,top_k,prefix,variant,dtype", [
+    (1, 1, 1, 128, 1, 0, "anchor", torch.bfloat16), (2, 300, 3, 200, 1, 0, "mean", torch.bfloat16),
+    (1, 700, 2, 1111, 2, 128, "anchor", torch.float32), (1, 1500, 5, 640, 3, 0, "anchor", torch.bfloat16)])
+def test_forward_block_is_its_steps(cuda_dev, B, N, H, C, top_k, prefix, variant, dtype):
+    c = block_case(B, N, H, C, 200, dtype)
+    want = by_steps(c, top_k, prefix, variant)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = bsa.forward_block(**c, top_k=top_k, prefix=prefix, variant=variant, dev_status=status)
+    assert torch.equal(got, want) and int(status) == 0
+    x = c["x"].clone()                   # the residual stream updated in place
+    assert bsa.forward_block(**dict(c, x=x), top_k=top_k, prefix=prefix, variant=variant, out=x) is x
+    assert torch.equal(x, want)
+
+
+def test_forward_block_against_the_oracles(cuda_dev):
+    """Every key block listed, so the attention is dense and exact.  The int8 rows of z are those of the oracle up
+    to ties; q, k, v, O and y are bf16 (2^-9 of a value each, in the mean), the attention's own bound is 1e-2, and
+    an O that is off by e moves the codes of a share e / step of its values by a step of 1/40 of the deviation:
+    sqrt(0.025 * 0.005), about 1e-2.  Together below 3e-2 of what the block adds to x."""
+    B, N, H, C = 1, 260, 2, 320
+    c = block_case(B, N, H, C, 300, torch.float32)
+    out = bsa.forward_block(**c, top_k=3)
+    n = {k: host(v) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+    _, z = orb.gate_norm(n["x"], scale=n["scale"][:, None], shift=n["shift"][:, None], pre="layer")
+    a, sa = orb.quantize_int8(z[0])
+    qkv = orb.linear_int8(a, sa, n["w_qkv"], n["s_qkv"].astype(np.float32), n["b_qkv"]).reshape(N, 3, H, 128).transpose(1, 2, 0, 3)
+    pos = n["positions"].astype(np.int64)
+    q, k = (orb.rotary(qkv[i], pos, n["freqs"], "interleaved", [22, 21, 21], n[w], 1e-6, 1.0) for i, w in ((0, "q_weight"), (1, "k_weight")))
+    s = q @ k.transpose(0, 2, 1) / np.sqrt(128)
+    pr = np.exp(s - s.max(-1, keepdims=True))
+    O = (pr / pr.sum(-1, keepdims=True)) @ qkv[2]
+    o8, so = orb.quantize_int8(O.transpose(1, 0, 2).reshape(N, H * 128))
+    y = orb.linear_int8(o8, so, n["w_out"], n["s_out"].astype(np.float32), n["b_out"])
+    h, _ = orb.gate_norm(n["x"][0], y, n["gate"], pre="none", post="rms", post_weight=n["post_weight"])
+    added, want = host(out[0]) - n["x"][0], h - n["x"][0]
+    assert np.linalg.norm(added - want) <= 3e-2 * np.linalg.norm(want)
+
+
+def test_two_streams_at_once(cuda_dev):
+    # the same calls on two streams with their own workspaces: nothing of one shows in the other
+    cs = [block_case(1, 900, 3, 512, s) for s in (400, 500)]
+    want = [by_steps(c, 2, 0, "anchor") for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = [[], []]
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            got[i].append(bsa.forward_block(**c, top_k=2, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g, want[i])
