@@ -576,8 +576,12 @@ def _elsewhere(device, stream, where):
     return torch.cuda.stream(stream)
 
 
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here(device, stream):
-    return stream is None and torch._C._cuda_getDevice() == device
+    return stream is None and _device_now() == device
 
 
 def _vector(g, n, where):
@@ -587,10 +591,6 @@ def _vector(g, n, where):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -625,8 +625,8 @@ def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_lengt
 
 @functools.lru_cache(maxsize=256)
 def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inverse, out_dtype):
-    """(device, output shapes and types, launches): a launch is the filled struct and the indices of
-    the tensors it takes (those that share their layout)."""
+    """(device, output shapes and types, launches): a launch is the filled struct and which of q, k
+    and v it takes (those that share their layout)."""
     where = "rotary"
     given = [g for g in parts if g is not None]
     _need(given and len(outs) == 3 and pos is not None and fr is not None, where)
@@ -666,7 +666,7 @@ def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inver
                               (_i32 * 4)(*pairs), int(inverse), DTYPES[dtype], DTYPES[odtype],
                               scale, eps, stride[0], stride[1], stride[2], ostride[0], ostride[1],
                               ostride[2], pos_b, pstride[-2])
-        launches.append((ctypes.byref(p), tuple(ids)))
+        launches.append((ctypes.byref(p), tuple(i in ids for i in range(3))))
     return device, tuple(want), tuple(launches)
 
 
@@ -683,21 +683,25 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
         (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions), _sig(freqs),
         (_sig(q_weight), _sig(k_weight)), layout,
         None if axis_pairs is None else tuple(axis_pairs), eps, scale, bool(inverse), out_dtype)
-    if not _here(device, stream):
+    if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "rotary"):
             return rotary(q, k, v, positions, freqs, layout, axis_pairs, q_weight, k_weight, eps,
                           scale, inverse, out, out_dtype)
     where = freqs.device
-    outs = [y if w is None or y is not None else _new(w[0], w[1], dtype=w[2], device=where)
-            for w, y in zip(want, outs)]
-    qkv, weights, st = (q, k, v), (q_weight, k_weight, None), _raw_stream(device)
-    for p, ids in launches:
-        a, w, o = [None] * 3, [None] * 3, [None] * 3
-        for i in ids:
-            a[i], w[i], o[i] = qkv[i].data_ptr(), _addr(weights[i]), outs[i].data_ptr()
-        _check(lib().bsa_rotary(p, *a, positions.data_ptr(), freqs.data_ptr(), w[0], w[1], *o, st),
-               "bsa_rotary")
-    return tuple(outs)
+    Q, K, V = [y if w is None or y is not None else _new(w[0], w[1], dtype=w[2], device=where)
+               for w, y in zip(want, outs)]
+    call, st = lib().bsa_rotary, _raw_stream(device)
+    at, fr = positions.data_ptr(), freqs.data_ptr()
+    for p, (i, j, k_) in launches:
+        rc = call(p, q.data_ptr() if i else None, k.data_ptr() if j else None,
+                  v.data_ptr() if k_ else None, at, fr,
+                  q_weight.data_ptr() if i and q_weight is not None else None,
+                  k_weight.data_ptr() if j and k_weight is not None else None,
+                  Q.data_ptr() if i else None, K.data_ptr() if j else None,
+                  V.data_ptr() if k_ else None, st)
+        if rc:
+            raise BsaError(rc, "bsa_rotary")
+    return Q, K, V
 
 
 def _mod(g, B, N, C, where):
@@ -757,24 +761,26 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
         (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out), pre,
         post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z)
-    if not _here(device, stream):
+    if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "gate_norm"):
             return gate_norm(x, y, gate, scale, shift, pre, pre_weight, pre_bias, post, post_weight,
                              post_bias, eps, residual_scale, branch_scale, quantize, z_dtype, h_out,
                              want_z)
     h, z, zs = h_out, None, None
     if h is None and y is not None:
-        h = _new(*shape, dtype=x.dtype, device=x.device)
+        h = _new(shape[0], shape[1], dtype=x.dtype, device=x.device)
     if want_z and quantize:
-        z = _new(*codes, dtype=torch.int8, device=x.device)
+        z = _new(codes[0], codes[1], dtype=torch.int8, device=x.device)
         zs = _new(codes[0][:1], (1,), dtype=torch.float32, device=x.device)
     elif want_z:
-        z = _new(*shape, dtype=z_dtype, device=x.device)
-    i = bsa_gate_norm_inputs(x.data_ptr(), _addr(y), _addr(gate), _addr(scale), _addr(shift),
-                             _addr(post_weight), _addr(post_bias), _addr(pre_weight),
-                             _addr(pre_bias))
-    _check(lib().bsa_gate_norm(p, ctypes.byref(i), _addr(h), _addr(z), _addr(zs),
-                               _raw_stream(device)), "bsa_gate_norm")
+        z = _new(shape[0], shape[1], dtype=z_dtype, device=x.device)
+    i = bsa_gate_norm_inputs(*[None if t is None else t.data_ptr() for t in (
+        x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias)])
+    rc = lib().bsa_gate_norm(p, ctypes.byref(i), None if h is None else h.data_ptr(),
+                             None if z is None else z.data_ptr(),
+                             None if zs is None else zs.data_ptr(), _raw_stream(device))
+    if rc:
+        raise BsaError(rc, "bsa_gate_norm")
     if zs is not None:
         z = (z if ld == C else z[:, :C], zs)
     return (x if h is None else h), z

@@ -10,13 +10,12 @@
 // HBM-bound: x and y are read once and h and z written once.  All sums and
 // statistics are fp32, z is formed from the unrounded h.
 //
-// Two kernels.  gate_norm_ring_kernel for many aligned rows whose vectors are
-// shared by the tokens: one CTA per SM keeps the vectors folded together in
+// Two kernels.  gate_norm_ring_kernel for many aligned rows: one CTA per SM keeps the vectors folded together in
 // shared memory (three or four loads a row saved), a producer warp streams
 // rows through a ring of shared-memory stages with bulk copies, and several
 // groups of warps each take the next row, so that the loads in flight do not
 // depend on registers and one group's reductions hide behind another's work.
-// gate_norm_kernel for the rest: one CTA a row, the row in registers between
+// Vectors with an entry a token are streamed like the rows.  gate_norm_kernel for the rest: one CTA a row, the row in registers between
 // its sums, the vectors from L1 / L2.
 #include <type_traits>
 
@@ -25,6 +24,9 @@
 
 #ifndef RINGK
 #define RINGK 4
+#endif
+#ifndef ROWS2
+#define ROWS2 (148 * 2)
 #endif
 namespace bsa {
 
@@ -112,6 +114,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const Gate
     if (kMode == kShifted) g.shift = static_cast<int>((b * a.x_b + t * a.x_n) & 7);
     float h[CH][8];
     load_row<CH, kMode>(g, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, a.C, h);
+    // with one chunk a thread there is room to have the vectors under way with the row
+    constexpr bool kEarly = CH == 1;
+    float mg[8], ms[8], mt[8];
+    if (kEarly) {
+      if (a.gate) load_mod8<kMode>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.gate_n != 0, a.C, 0, mg);
+      if (a.mscale) load_mod8<kMode>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.scale_n != 0, a.C, 0, ms);
+      if (a.shift) load_mod8<kMode>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.shift_n != 0, a.C, 0, mt);
+    }
     if (a.y) {
       float y[CH][8];
       const int64_t o = b * a.y_b + t * a.y_n;
@@ -124,7 +134,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const Gate
       for (int c = 0; c < CH; ++c) {
         if (a.gate) {
           float m[8];
-          load_mod8<kMode>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.gate_n != 0, a.C, c, m);
+          if (!kEarly)
+            load_mod8<kMode>(g, a.gate, a.mod_fp32, b * a.gate_b + t * a.gate_n, a.gate_n != 0, a.C, c, m);
+          else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m[j] = mg[j];
 #pragma unroll
           for (int j = 0; j < 8; ++j) y[c][j] *= m[j];
         }
@@ -143,13 +157,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const Gate
     for (int c = 0; c < CH; ++c) {
       if (a.mscale) {
         float m[8];
-        load_mod8<kMode>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.scale_n != 0, a.C, c, m);
+        if (!kEarly)
+          load_mod8<kMode>(g, a.mscale, a.mod_fp32, b * a.scale_b + t * a.scale_n, a.scale_n != 0, a.C, c, m);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m[j] = ms[j];
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] = fmaf(h[c][j], m[j], h[c][j]);
       }
       if (a.shift) {
         float m[8];
-        load_mod8<kMode>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.shift_n != 0, a.C, c, m);
+        if (!kEarly)
+          load_mod8<kMode>(g, a.shift, a.mod_fp32, b * a.shift_b + t * a.shift_n, a.shift_n != 0, a.C, c, m);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m[j] = mt[j];
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[c][j] += m[j];
       }
@@ -188,7 +210,10 @@ struct RingShape {
   int rows, log_rows;            // rows a stage: one copy brings them where they are contiguous
   int has_gain, has_post_bias;   // gate * post_weight, gate * post_bias
   int has_a, has_b;              // pre_weight (1 + scale), pre_bias (1 + scale) + shift
+  int tok_gate, tok_mod;         // gate, scale and shift with a vector a token: streamed with the rows
+  uint32_t m_bytes, gate_at, scale_at, shift_at;   // of such a vector; where a stage has them
   uint32_t x_bytes, y_bytes;     // of a row
+  uint32_t row_bytes;            // of a row and the vectors that come with it
   uint32_t stage_bytes, y_at;    // of a stage; where its rows of y start
   uint32_t off_stage, off_red, off_ctl, bytes;
 };
@@ -226,6 +251,13 @@ __device__ __forceinline__ void smem8(const float* p, Oct& v) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v.p[0] = make_float2(a.x, a.y), v.p[1] = make_float2(a.z, a.w);
   v.p[2] = make_float2(b.x, b.y), v.p[3] = make_float2(b.z, b.w);
+}
+
+__device__ __forceinline__ void smem8_mod(const uint8_t* p, int fp32, int i, Oct& v) {
+  if (fp32)
+    smem8(reinterpret_cast<const float*>(p) + i, v);
+  else
+    smem8(reinterpret_cast<const __nv_bfloat16*>(p) + i, v);
 }
 
 // A vector folded in shared memory: the 8 values of 32 neighbouring threads
@@ -336,12 +368,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
         const int64_t t = static_cast<int64_t>(q) * s.rows;
         const uint32_t n = static_cast<uint32_t>(a.N - t < s.rows ? a.N - t : s.rows);
         uint8_t* dst = sm + s.off_stage + st * s.stage_bytes;
-        mbar_arrive_expect_tx(&ctl->full[st], n * (s.x_bytes + s.y_bytes));
+        mbar_arrive_expect_tx(&ctl->full[st], n * s.row_bytes);
         bulk_load(dst, static_cast<const Tx*>(a.x) + b * a.x_b + t * a.x_n, n * s.x_bytes,
                   &ctl->full[st]);
         if (s.y_bytes)
           bulk_load(dst + s.y_at, static_cast<const Ty*>(a.y) + b * a.y_b + t * a.y_n,
                     n * s.y_bytes, &ctl->full[st]);
+        auto vector = [&](uint32_t at, const void* p, int64_t o) {
+          bulk_load(dst + at, static_cast<const char*>(p) + o * (a.mod_fp32 ? 4 : 2), n * s.m_bytes,
+                    &ctl->full[st]);
+        };
+        if (s.tok_gate) vector(s.gate_at, a.gate, b * a.gate_b + t * a.gate_n);
+        if (s.tok_mod && a.mscale) vector(s.scale_at, a.mscale, b * a.scale_b + t * a.scale_n);
+        if (s.tok_mod && a.shift) vector(s.shift_at, a.shift, b * a.shift_b + t * a.shift_n);
         if (++st == static_cast<uint32_t>(s.stages)) st = 0, ++round;
       }
       // every issued load has landed before the CTA exits
@@ -373,9 +412,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     };
     for (int i = 8 * threadIdx.x; i < C; i += 8 * rows_threads) {
       float gt[8], sc[8], sh[8], w[8], o[8];
-      mod(a.gate, b * a.gate_b, i, 1.f, gt);
-      mod(a.mscale, b * a.scale_b, i, 0.f, sc);
-      mod(a.shift, b * a.shift_b, i, 0.f, sh);
+      mod(s.tok_gate ? nullptr : a.gate, b * a.gate_b, i, 1.f, gt);
+      mod(s.tok_mod ? nullptr : a.mscale, b * a.scale_b, i, 0.f, sc);
+      mod(s.tok_mod ? nullptr : a.shift, b * a.shift_b, i, 0.f, sh);
 #pragma unroll
       for (int j = 0; j < 8; ++j) gt[j] *= a.branch_scale, sc[j] += 1.f, w[j] = 1.f;
       if (s.has_gain) {
@@ -440,6 +479,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     uint64_t* empty = &ctl->empty[st];
     const Tx* xs = reinterpret_cast<const Tx*>(stage + sub * s.x_bytes);
     const Ty* ys = reinterpret_cast<const Ty*>(stage + s.y_at + sub * s.y_bytes);
+    const uint8_t* ms = stage + sub * s.m_bytes;
     sub += s.groups;
     const uint32_t on = sub >> s.log_rows;
     sub &= s.rows - 1;
@@ -474,6 +514,15 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
           for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
         }
       }
+      if (s.tok_gate) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+          Oct m;
+          smem8_mod(ms + s.gate_at, a.mod_fp32, at[c], m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[c].p[j] = mul2(h[c].p[j], m.p[j]);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         Oct x;
@@ -481,7 +530,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(x.p[j], pair(a.residual_scale), h[c].p[j]);
       }
-      mbar_arrive(empty);
+      if (!s.tok_mod) mbar_arrive(empty);
       if (a.h) {
         Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
 #pragma unroll
@@ -491,7 +540,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c) smem8(xs + at[c], h[c]);
-      mbar_arrive(empty);
+      if (!s.tok_mod) mbar_arrive(empty);
     }
     if (!a.z) continue;
     const float2 mr =
@@ -517,6 +566,23 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
       }
+    }
+    if (s.tok_mod) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Oct m;
+        if (a.mscale) {
+          smem8_mod(ms + s.scale_at, a.mod_fp32, at[c], m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(h[c].p[j], m.p[j], h[c].p[j]);
+        }
+        if (a.shift) {
+          smem8_mod(ms + s.shift_at, a.mod_fp32, at[c], m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
+        }
+      }
+      mbar_arrive(empty);
     }
     const int64_t o = b * a.z_b + t * a.z_n;
     if (a.z_type == kTypeBf16) {
@@ -564,8 +630,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
 // that are short (their loads are in flight enough with one CTA a row), few,
 // or too long for two of them beside the vectors in shared memory.
 bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3* grid) {
-  const bool token = (a.gate && a.gate_n) || (a.mscale && a.scale_n) || (a.shift && a.shift_n);
-  if (token) return false;
+  // scale and shift both once a batch entry (folded) or both once a token (streamed)
+  const bool tok_scale = a.mscale && a.scale_n, tok_shift = a.shift && a.shift_n;
+  s->tok_mod = tok_scale || tok_shift;
+  if (s->tok_mod && ((a.mscale && !tok_scale) || (a.shift && !tok_shift))) return false;
+  s->tok_gate = a.gate && a.gate_n;
+  s->m_bytes = static_cast<uint32_t>(a.C) * (a.mod_fp32 ? 4 : 2);
   const int per = 148 / a.B > 0 ? 148 / a.B : 1;
   s->x_bytes = static_cast<uint32_t>(a.C) * (x_fp32 ? 4 : 2);
   s->y_bytes = a.y ? static_cast<uint32_t>(a.C) * (a.y_fp32 ? 4 : 2) : 0;
@@ -578,21 +648,26 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   if (a.N < RINGK * per * s->groups || a.B > 65535) return false;
   // short rows: 8 KB a stage and one copy for it, where they lie one after another
   s->rows = 1, s->log_rows = 0;
-  if (a.x_n == a.C && (!a.y || a.y_n == a.C))
-    while (s->rows < 16 && s->rows * (s->x_bytes + s->y_bytes) < 8192)
-      s->rows *= 2, ++s->log_rows;
-  if (s->rows * (s->x_bytes + s->y_bytes) < 4096) return false;
-  s->has_gain = a.y && (a.gate || a.post_weight || a.branch_scale != 1.f);
+  s->row_bytes = s->x_bytes + s->y_bytes +
+                 (s->tok_gate + (s->tok_mod ? !!a.mscale + !!a.shift : 0)) * s->m_bytes;
+  const bool dense = a.x_n == a.C && (!a.y || a.y_n == a.C) && (!s->tok_gate || a.gate_n == a.C) &&
+                     (!s->tok_mod || ((!a.mscale || a.scale_n == a.C) && (!a.shift || a.shift_n == a.C)));
+  while (dense && s->rows < 16 && s->rows * s->row_bytes < 8192) s->rows *= 2, ++s->log_rows;
+  if (s->rows * s->row_bytes < 4096) return false;
+  s->has_gain = a.y && ((a.gate && !s->tok_gate) || a.post_weight || a.branch_scale != 1.f);
   s->has_post_bias = a.y && a.post_bias;
-  s->has_a = a.z && (a.mscale || a.pre_weight);
-  s->has_b = a.z && (a.shift || a.pre_bias);
+  s->has_a = a.z && ((a.mscale && !s->tok_mod) || a.pre_weight);
+  s->has_b = a.z && ((a.shift && !s->tok_mod) || a.pre_bias);
   const uint32_t vectors =
       (s->has_gain + s->has_post_bias + s->has_a + s->has_b) * ((a.C + 255) & ~255) * 4u;
   s->off_stage = (vectors + 127) & ~127u;
   const uint32_t fixed = s->groups * static_cast<uint32_t>(sizeof(RowReduce)) + sizeof(RingCtl) + 16;
-  const uint32_t stage = s->rows * (s->x_bytes + s->y_bytes);
+  const uint32_t stage = s->rows * s->row_bytes;
   s->stage_bytes = stage;
   s->y_at = s->rows * s->x_bytes;
+  s->gate_at = s->y_at + s->rows * s->y_bytes;
+  s->scale_at = s->gate_at + (s->tok_gate ? s->rows * s->m_bytes : 0);
+  s->shift_at = s->scale_at + (s->tok_mod && a.mscale ? s->rows * s->m_bytes : 0);
   if (s->off_stage + fixed + 2 * stage > kRingSmem) return false;
   int stages = static_cast<int>((kRingSmem - s->off_stage - fixed) / stage);
   s->stages = stages < kMaxStages ? stages : kMaxStages;
@@ -639,10 +714,10 @@ cudaError_t launch(const GateNormArgs& a, int ch, int threads, int blocks, cudaS
 }  // namespace
 
 // Threads and chunks (1, 2 or 4) of a row of n <= 32,768 values: two chunks a
-// thread, one for short rows and for few rows, where a row's latency counts.
+// thread, one for short rows and where a row's latency counts (few rows).
 void row_shape(int n, int64_t rows, int* ch, int* threads) {
   const int vecs = (n + 7) / 8;
-  int c = rows >= 148 * 2 ? 2 : 1;
+  int c = rows >= ROWS2 ? 2 : 1;
   while (c > 1 && (vecs + c - 1) / c < 32) c /= 2;
   while ((vecs + c - 1) / c > 1024) c *= 2;
   *ch = c;

@@ -115,36 +115,70 @@ __device__ __forceinline__ void load_row(const RowGroup& g, const T* p, int n, f
   }
 }
 
-// One chunk of a vector that many rows share (kept in L1); it starts on 16
-// bytes itself, so that only kAligned chunks do.
-template <int kMode>
-__device__ __forceinline__ void load_shared8(const RowGroup& g, const float* p, int n, int c, float v[8]) {
-  if (kMode == kAligned) {
-    const int i = row_index<kMode>(g, c, 0);
-    float4 a = make_float4(0, 0, 0, 0), b = a;
-    if (i < n) {
-      a = __ldg(reinterpret_cast<const float4*>(p + i));
-      b = __ldg(reinterpret_cast<const float4*>(p + i + 4));
-    }
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = row_in<kMode>(g, c, j, n) ? __ldg(p + row_index<kMode>(g, c, j)) : 0.f;
-  }
+__device__ __forceinline__ void shared_words(const float* p, float v[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-template <int kMode>
-__device__ __forceinline__ void load_shared8(const RowGroup& g, const __nv_bfloat16* p, int n, int c,
-                                             float v[8]) {
-  if (kMode == kAligned) {
-    const int i = row_index<kMode>(g, c, 0);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (i < n) w = __ldg(reinterpret_cast<const uint4*>(p + i));
-    bf16x8_to_f32(w, v);
+__device__ __forceinline__ void shared_words(const __nv_bfloat16* p, float v[8]) {
+  bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+// 8 neighbours at p, which starts anywhere: from the aligned words around them
+// (which lie inside the vector: `room` says so) by a shift that all threads of
+// the row share.  8 scalar loads 32 bytes apart across a warp would be 64 passes
+// through L1, these are 24.
+__device__ __forceinline__ void around8(const float* p, float v[8]) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 2) & 3u;
+  const float4* q = reinterpret_cast<const float4*>(p - off);
+  const float4 a = __ldg(q), b = __ldg(q + 1);
+  float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (off) c = __ldg(q + 2);
+  float w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int j = 0; j < 10; ++j) w[j] = off & 2u ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = off & 1u ? w[j + 1] : w[j];
+}
+__device__ __forceinline__ bool room(const float* p, int i, int n) {
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p + i) >> 2) & 3u);
+  return i >= off && i - off + (off ? 12 : 8) <= n;
+}
+__device__ __forceinline__ void around8(const __nv_bfloat16* p, float v[8]) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 7u;
+  const uint4* q = reinterpret_cast<const uint4*>(p - off);
+  const uint4 a = __ldg(q);
+  uint4 b = make_uint4(0, 0, 0, 0);
+  if (off) b = __ldg(q + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = off & 4u ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = off & 2u ? w[j + 1] : w[j];
+  uint4 r;
+  r.x = off & 1u ? __funnelshift_r(w[0], w[1], 16) : w[0];
+  r.y = off & 1u ? __funnelshift_r(w[1], w[2], 16) : w[1];
+  r.z = off & 1u ? __funnelshift_r(w[2], w[3], 16) : w[2];
+  r.w = off & 1u ? __funnelshift_r(w[3], w[4], 16) : w[3];
+  bf16x8_to_f32(r, v);
+}
+__device__ __forceinline__ bool room(const __nv_bfloat16* p, int i, int n) {
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p + i) >> 1) & 7u);
+  return i >= off && i - off + (off ? 16 : 8) <= n;
+}
+
+// One chunk of a vector that many rows share (kept in L1); it starts where its
+// batch entry does, so that only kAligned chunks start on 16 bytes.
+template <int kMode, class T>
+__device__ __forceinline__ void load_shared8(const RowGroup& g, const T* p, int n, int c, float v[8]) {
+  const int i = row_index<kMode>(g, c, 0);
+  if (kMode == kAligned && i < n) {
+    shared_words(p + i, v);
+  } else if (kMode == kShifted && i >= 0 && room(p, i, n)) {
+    around8(p + i, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      v[j] = row_in<kMode>(g, c, j, n) ? to_f32(p[row_index<kMode>(g, c, j)]) : 0.f;
+      v[j] = kMode != kAligned && row_in<kMode>(g, c, j, n) ? to_f32(p[row_index<kMode>(g, c, j)]) : 0.f;
   }
 }
 

@@ -434,13 +434,17 @@ RING = [
     (1, 601, 1024, "none", "rms", torch.float32, torch.float32, "c", False),
     (150, 5, 2048, "rms", "rms", torch.bfloat16, torch.bfloat16, "b", True),
     (1, 593, 12288, "layer", "none", torch.bfloat16, torch.bfloat16, "c", False),
+    (1, 2500, 7168, "layer", "rms", torch.bfloat16, torch.bfloat16, "n", True),
+    (2, 2700, 520, "rms", "layer", torch.float32, torch.bfloat16, "n", True),
+    (1, 13000, 256, "layer", "rms", torch.bfloat16, torch.bfloat16, "n", False),
+    (1, 13003, 136, "rms", "rms", torch.bfloat16, torch.bfloat16, "b", True),
 ]
 
 
 @pytest.mark.parametrize("B,N,C,pre,post,tx,ty,shape,aff", RING)
 def test_gate_norm_of_many_rows(cuda_dev, B, N, C, pre, post, tx, ty, shape, aff):
     x, y = rnd(90, B, N, C, dtype=tx) + 3, rnd(91, B, N, C, dtype=ty) - 2
-    s = dict(b=(B, C), b1=(B, 1, C), c=(C,))[shape]
+    s = dict(b=(B, C), b1=(B, 1, C), c=(C,), n=(B, N, C))[shape]
     gate, scale, shift = (rnd(92 + i, *s, dtype=torch.bfloat16, scale=0.5) for i in range(3))
     args = (x, y, gate, scale, shift, pre, post)
     h, z, ws = run_gate_norm(*args, aff, 1e-6, 0.5, 2.0)
