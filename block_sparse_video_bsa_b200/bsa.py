@@ -744,13 +744,13 @@ def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, re
         DTYPES[mods[0]] if mods else 1, 2 if quantize and want_z else DTYPES[z_dtype], eps,
         residual_scale, branch_scale, *_rows(x, C), *_rows(y, C), *h, N * ld, ld,
         *_mod(gate, B, N, C, where), *_mod(scale, B, N, C, where), *_mod(shift, B, N, C, where))
-    return device, ctypes.byref(p), ((B, N, C), (N * C, C, 1)), ((B * N, ld), (ld, 1)), C, ld
+    return device, p, ((B, N, C), (N * C, C, 1)), ((B * N, ld), (ld, 1)), C, ld
 
 
 def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weight=None,
               pre_bias=None, post="none", post_weight=None, post_bias=None, eps=1e-6,
               residual_scale=1.0, branch_scale=1.0, quantize=False, z_dtype=torch.bfloat16,
-              h_out=None, want_z=True, stream=None):
+              h_out=None, want_z=True, dev_status=None, stream=None):
     """bsa_gate_norm: (h, z) with h = residual_scale x + branch_scale gate post(y) (x itself without
     y) and z = pre(h) (1 + scale) + shift.
 
@@ -765,7 +765,11 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         with _elsewhere(device, stream, "gate_norm"):
             return gate_norm(x, y, gate, scale, shift, pre, pre_weight, pre_bias, post, post_weight,
                              post_bias, eps, residual_scale, branch_scale, quantize, z_dtype, h_out,
-                             want_z)
+                             want_z, dev_status)
+    if dev_status is not None:
+        _need(dev_status.get_device() == device, "gate_norm")
+        p = bsa_gate_norm_params.from_buffer_copy(p)
+        p.dev_status = dev_status.data_ptr()
     h, z, zs = h_out, None, None
     if h is None and y is not None:
         h = _new(shape[0], shape[1], dtype=x.dtype, device=x.device)
@@ -776,7 +780,7 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         z = _new(shape[0], shape[1], dtype=z_dtype, device=x.device)
     i = bsa_gate_norm_inputs(*[None if t is None else t.data_ptr() for t in (
         x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias)])
-    rc = lib().bsa_gate_norm(p, ctypes.byref(i), None if h is None else h.data_ptr(),
+    rc = lib().bsa_gate_norm(ctypes.byref(p), ctypes.byref(i), None if h is None else h.data_ptr(),
                              None if z is None else z.data_ptr(),
                              None if zs is None else zs.data_ptr(), _raw_stream(device))
     if rc:
@@ -846,6 +850,7 @@ def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out
     if not _here(device, stream):
         with _elsewhere(device, stream, "linear_int8"):
             return linear_int8(a, a_scale, w, w_scale, bias, out_dtype, out, dev_status)
+    _need(dev_status is None or dev_status.get_device() == device, "linear_int8")
     o = out
     if o is None:
         o = _new(p[:2], (p[1], 1), dtype=out_dtype, device=a.device)

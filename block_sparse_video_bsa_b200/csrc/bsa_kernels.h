@@ -220,7 +220,7 @@ struct QuantInt8Args {
 };
 cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cudaStream_t st);
 // Threads and 8-value chunks a thread of a row of n values (gate_norm.cu).
-void row_shape(int n, int64_t rows, int* ch, int* threads);
+void row_shape(int n, int64_t rows, int few, int* ch, int* threads);
 
 // int8 product (linear_int8.cu): out[m, n] = a_scale[m] w_scale[n] sum_k a[m, k] w[n, k] + bias[n].
 struct LinearInt8Args {

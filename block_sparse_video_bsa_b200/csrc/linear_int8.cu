@@ -244,7 +244,9 @@ cudaError_t go_few(const LinearInt8Args& a, const CUtensorMap& mw, const CUtenso
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mw, ma, a, split);
+  e = cudaLaunchKernelEx(&cfg, kernel, mw, ma, a, split);
+  if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next call
+  return e;
 }
 
 // ------------------------------------------------------------ CTA pairs

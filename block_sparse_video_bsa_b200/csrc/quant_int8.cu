@@ -107,7 +107,7 @@ cudaError_t launch(const QuantInt8Args& a, int ch, int threads, int blocks, cuda
 cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
   int ch, threads;
-  row_shape(a.S * a.L, rows, &ch, &threads);
+  row_shape(a.S * a.L, rows, 2 * 148, &ch, &threads);
   int blocks = static_cast<int>(rows < (1 << 30) ? rows : (1 << 30));
   if (vec && !x_fp32) {
     const int vecs = (a.S * a.L + 7) / 8;

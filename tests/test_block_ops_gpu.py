@@ -130,6 +130,24 @@ def test_rotary_leaves_the_rest_alone(cuda_dev):
         assert out[..., :50].isfinite().all()
 
 
+def test_rotary_of_no_dimension_changes_the_layout(cuda_dev):
+    qkv = rnd(15, 2, 19, 3, 5, 128, dtype=torch.bfloat16)
+    views = [qkv[:, :, i].transpose(1, 2) for i in range(3)]
+    pos, freqs = torch.zeros(19, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.float64, device="cuda")
+    for got, want in zip(bsa.rotary(*views, pos, freqs), views):
+        assert torch.equal(got, want) and got.is_contiguous()
+
+
+def test_rotary_positions_of_each_batch_entry_and_broadcast_rows(cuda_dev):
+    # strided positions [B, N, axes], and one row of q read for every token (stride 0)
+    B, H, N = 3, 2, 37
+    pos = torch.randint(0, 5000, (B, N, 4), device="cuda", dtype=torch.int32)[:, :, :3]
+    freqs, _ = bsa.rotary_freqs([10, 11, 11])
+    q = rnd(16, B, H, 1, 128).expand(B, H, N, 128)
+    Q, _, _ = bsa.rotary(q, None, None, pos, freqs, "interleaved", [10, 11, 11])
+    check_rotary(Q, q, pos, freqs, "interleaved", [10, 11, 11], None, 0, 1.0)
+
+
 def test_rotary_other_head_counts_and_streams(cuda_dev):
     q, k, v = rnd(8, 1, 8, 30, 128), rnd(9, 1, 2, 30, 128), rnd(10, 1, 2, 30, 128)
     pos = torch.arange(30, dtype=torch.int32, device="cuda")
@@ -465,6 +483,14 @@ def test_gate_norm_of_many_rows(cuda_dev, B, N, C, pre, post, tx, ty, shape, aff
     hr4, _, eh4, _ = gate_norm_bounds(x, y, None, None, None, pre, post, ws4, 1e-6, 1.0, 1.0)
     assert none is None
     close(h4, hr4, eh4)
+
+
+def test_gate_norm_reports_no_expired_wait(cuda_dev):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = rnd(97, 1, 3000, 2048, dtype=torch.bfloat16)
+    _, a = bsa.gate_norm(x)
+    _, b = bsa.gate_norm(x, dev_status=status)
+    assert torch.equal(a, b) and int(status) == 0
 
 
 def test_gate_norm_of_many_rows_in_wider_buffers(cuda_dev):
