@@ -666,6 +666,10 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   if (s->off_stage + fixed + 2 * stage > kRingSmem) return false;
   int stages = static_cast<int>((kRingSmem - s->off_stage - fixed) / stage);
   s->stages = stages < kMaxStages ? stages : kMaxStages;
+  // A group waits for its next row's stage by parity, so that stage's last
+  // filling must have landed before: rows are filled in turn and the group's own
+  // row before was, so the stages have to hold as many rows as there are groups.
+  if (s->groups > s->stages * s->rows) s->groups = s->stages * s->rows;
   s->off_red = (s->off_stage + s->stages * stage + 15) & ~15u;
   s->off_ctl = s->off_red + s->groups * static_cast<uint32_t>(sizeof(RowReduce));
   s->bytes = s->off_ctl + sizeof(RingCtl);

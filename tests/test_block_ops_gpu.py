@@ -456,14 +456,17 @@ RING = [
     (2, 2700, 520, "rms", "layer", torch.float32, torch.bfloat16, "n", True),
     (1, 13000, 256, "layer", "rms", torch.bfloat16, torch.bfloat16, "n", False),
     (1, 13003, 136, "rms", "rms", torch.bfloat16, torch.bfloat16, "b", True),
+    # two stages, fewer than the groups of warps that a CTA has room for
+    (2, 1000, 6992, "rms", "layer", torch.bfloat16, torch.bfloat16, "nf", False),
+    (1, 2000, 4816, "none", "rms", torch.float32, torch.float32, "nf", False),
 ]
 
 
 @pytest.mark.parametrize("B,N,C,pre,post,tx,ty,shape,aff", RING)
 def test_gate_norm_of_many_rows(cuda_dev, B, N, C, pre, post, tx, ty, shape, aff):
     x, y = rnd(90, B, N, C, dtype=tx) + 3, rnd(91, B, N, C, dtype=ty) - 2
-    s = dict(b=(B, C), b1=(B, 1, C), c=(C,), n=(B, N, C))[shape]
-    gate, scale, shift = (rnd(92 + i, *s, dtype=torch.bfloat16, scale=0.5) for i in range(3))
+    s = dict(b=(B, C), b1=(B, 1, C), c=(C,), n=(B, N, C), nf=(B, N, C))[shape]
+    gate, scale, shift = (rnd(92 + i, *s, dtype=torch.float32 if shape == "nf" else torch.bfloat16, scale=0.5) for i in range(3))
     args = (x, y, gate, scale, shift, pre, post)
     h, z, ws = run_gate_norm(*args, aff, 1e-6, 0.5, 2.0)
     hr, zr, eh, ez = gate_norm_bounds(*args, ws, 1e-6, 0.5, 2.0)
