@@ -166,7 +166,7 @@ int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inpu
       !std::isfinite(p->branch_scale))
     return BSA_ERR_INVALID;
   if (!in->x || (!h && !z)) return BSA_ERR_INVALID;
-  if (!in->y && (h || in->gate || in->post_weight || in->post_bias)) return BSA_ERR_INVALID;
+  if (!in->y && (h || in->gate)) return BSA_ERR_INVALID;
   if (!z && (in->scale || in->shift || in->pre_weight || in->pre_bias)) return BSA_ERR_INVALID;
   if ((z && p->z_dtype == BSA_DTYPE_INT8) != (z_scale != nullptr)) return BSA_ERR_INVALID;
   // the stride of a single entry is never used
@@ -202,7 +202,8 @@ int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inpu
   if (rc) return rc;
   bsa::GateNormArgs a = {};
   a.x = in->x, a.y = in->y, a.gate = in->gate, a.mscale = in->scale, a.shift = in->shift;
-  a.post_weight = in->post_weight, a.post_bias = in->post_bias;
+  a.post_weight = in->y ? in->post_weight : nullptr;
+  a.post_bias = in->y ? in->post_bias : nullptr;
   a.pre_weight = in->pre_weight, a.pre_bias = in->pre_bias;
   a.h = h, a.z = z, a.z_scale = z_scale;
   a.B = p->B, a.N = p->N, a.C = p->C, a.pre = p->pre, a.post = p->post;

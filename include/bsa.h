@@ -608,7 +608,8 @@ typedef struct {
  *   z = pre(h) (1 + scale) + shift
  * post and pre: nothing, v rsqrt(mean(v^2) + eps), or (v - mean(v))
  * rsqrt(mean((v - mean(v))^2) + eps), then weight and bias where given.  z is
- * formed from h before its rounding.  h is written when non-NULL (it needs y),
+ * formed from h before its rounding.  Without y the norm post and its weights are
+ * not looked at.  h is written when non-NULL (it needs y),
  * z when non-NULL.  z_dtype int8: codes and z_scale [B N] as
  * bsa_quantize_int8 makes them; z_scale is NULL otherwise.  h may be x with
  * the same strides (in place). */

@@ -488,6 +488,14 @@ def test_gate_norm_of_many_rows(cuda_dev, B, N, C, pre, post, tx, ty, shape, aff
     close(h4, hr4, eh4)
 
 
+@pytest.mark.parametrize("N", [20, 1300])
+def test_gate_norm_without_a_branch_ignores_its_norm(cuda_dev, N):
+    x, w = rnd(98, 1, N, 2048, dtype=torch.bfloat16), rnd(99, 2048)
+    _, a = bsa.gate_norm(x, post="layer", post_weight=w, post_bias=w)
+    _, b = bsa.gate_norm(x)
+    assert torch.equal(a, b)
+
+
 def test_gate_norm_reports_no_expired_wait(cuda_dev):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     x = rnd(97, 1, 3000, 2048, dtype=torch.bfloat16)
