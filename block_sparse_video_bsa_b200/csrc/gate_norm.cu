@@ -468,8 +468,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
   for (;;) {
     if (q >= blocks) break;
     const int64_t t = static_cast<int64_t>(q) * s.rows + sub;
-    // the whole group goes on or none of it
-    if (!g.all(mbar_wait(&ctl->full[st], round & 1, wc))) break;
+    // A wait by parity tells a filling from the next one only: rows of a stage go
+    // to different groups and loads land in any order, so this group first sees
+    // that the stage's last filling was read (it was asked for before this group's
+    // own last row, so its phase is the current one at most), then that this one
+    // has landed.  The whole group goes on or none of it.
+    const bool read = round == 0 || mbar_wait(&ctl->empty[st], (round - 1) & 1, wc);
+    if (!g.all(read && mbar_wait(&ctl->full[st], round & 1, wc))) break;
     const uint8_t* stage = sm + s.off_stage + st * s.stage_bytes;
     uint64_t* empty = &ctl->empty[st];
     const Tx* xs = reinterpret_cast<const Tx*>(stage + sub * s.x_bytes);
@@ -666,9 +671,9 @@ bool ring_shape(const GateNormArgs& a, bool x_fp32, RingShape* s, int* ch, dim3*
   if (s->off_stage + fixed + 2 * stage > kRingSmem) return false;
   int stages = static_cast<int>((kRingSmem - s->off_stage - fixed) / stage);
   s->stages = stages < kMaxStages ? stages : kMaxStages;
-  // A group waits for its next row's stage by parity, so that stage's last
-  // filling must have landed before: rows are filled in turn and the group's own
-  // row before was, so the stages have to hold as many rows as there are groups.
+  // A group waits for its next row's stage by parity: the stage's last filling
+  // has to be asked for before the group's own last row was (the kernel's waits),
+  // so the stages have to hold as many rows as there are groups.
   if (s->groups > s->stages * s->rows) s->groups = s->stages * s->rows;
   s->off_red = (s->off_stage + s->stages * stage + 15) & ~15u;
   s->off_ctl = s->off_red + s->groups * static_cast<uint32_t>(sizeof(RowReduce));

@@ -496,6 +496,19 @@ def test_gate_norm_without_a_branch_ignores_its_norm(cuda_dev, N):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("N,C,dtype", [(23567, 2552, torch.float32), (37740, 1024, torch.bfloat16), (30000, 512, torch.bfloat16), (20000, 5120, torch.bfloat16)])
+def test_gate_norm_streams_rows_in_order(cuda_dev, N, C, dtype):
+    # without norms nothing but the stages' barriers holds the groups of warps together: every value is exact,
+    # over many calls
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x, y = rnd(100, 1, N, C, dtype=dtype), rnd(101, 1, N, C, dtype=torch.bfloat16)
+    want = (x.float() + y.float()).to(dtype)
+    for _ in range(40):
+        h, z = bsa.gate_norm(x, y, pre="none", post="none", dev_status=status)
+        assert torch.equal(h, want) and torch.equal(z, (x.float() + y.float()).bfloat16())
+    assert int(status) == 0
+
+
 def test_gate_norm_reports_no_expired_wait(cuda_dev):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     x = rnd(97, 1, 3000, 2048, dtype=torch.bfloat16)
