@@ -66,11 +66,24 @@ __device__ __forceinline__ void put8(float* p, const float x[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// The exchange buffer: a gap after every 8 values and rows of 152, so that a
+// warp's four rows of eight lanes, 8 values apart, meet every bank once.
+constexpr int kXchRow = 152;
+__device__ __forceinline__ int xch_at(int e) { return e + (e >> 3); }
+
+template <class Tin, int kMode>
+constexpr int rotary_smem() {
+  using W = Words<Tin, kMode>;
+  return W::kDepth * 2 * W::kPerChunk * kThreads * 16 +
+         (kMode == kHalfAny ? kRows * kXchRow * 4 : 0);
+}
+
 template <class Tin, class Tout, int kMode>
-__global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a) {
   constexpr int kW = Words<Tin, kMode>::kPerChunk, kDepth = Words<Tin, kMode>::kDepth;
-  __shared__ uint4 ring[kDepth][2 * kW][kThreads];
-  __shared__ float xch[kMode == kHalfAny ? kRows : 1][kMode == kHalfAny ? kDim : 1];
+  extern __shared__ uint4 dyn[];
+  uint4 (*ring)[2 * kW][kThreads] = reinterpret_cast<uint4 (*)[2 * kW][kThreads]>(dyn);
+  float (*xch)[kXchRow] = reinterpret_cast<float (*)[kXchRow]>(dyn + kDepth * 2 * kW * kThreads);
   const int lane = threadIdx.x & (kLanes - 1), row = threadIdx.x / kLanes;
   const int b = blockIdx.z / a.ntens, t = blockIdx.z % a.ntens;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * a.tt + (row & (a.tt - 1));
@@ -114,15 +127,25 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a)
   float c0[8], s0[8], c1[8], s1[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) c0[j] = c1[j] = 1.f, s0[j] = s1[j] = 0.f;
+  // Steps of all pairs, once a CTA: fp64 runs at about one operation a clock and
+  // SM, and a token of one head would need five for each of its pairs.  They lie
+  // in the ring's last slot, which is filled only after the second barrier.
+  uint64_t* steps64 = reinterpret_cast<uint64_t*>(&ring[kDepth - 1][0][0]);
+  if (turns) {
+    if (static_cast<int>(threadIdx.x) < half) {
+      const double f = __ldg(a.freqs + threadIdx.x) * 0.15915494309189533577;   // turns a position
+      steps64[threadIdx.x] =
+          static_cast<uint64_t>(__double2ll_rn((f - rint(f)) * 18446744073709551616.0));
+    }
+    __syncthreads();
+  }
   if (turns && live) {
     const int32_t* pos = a.positions + b * a.pos_b + n * a.pos_n;
     auto turn = [&](int i, float* sn, float* cs) {
       int axis = 0;
       while (i >= a.axis_end[axis]) ++axis;
-      const double f = __ldg(a.freqs + i) * 0.15915494309189533577;   // turns a position
-      const int64_t step = __double2ll_rn((f - rint(f)) * 18446744073709551616.0);
-      const uint64_t phase = static_cast<uint64_t>(step) *
-                             static_cast<uint64_t>(static_cast<int64_t>(__ldg(pos + axis)));
+      const uint64_t phase =
+          steps64[i] * static_cast<uint64_t>(static_cast<int64_t>(__ldg(pos + axis)));
       // [-2^31, 2^31) of a turn in 2^-32 units -> half turns in [-1, 1)
       sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, sn, cs);
       *cs *= a.scale;
@@ -165,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a)
       }
     }
   }
+  if (turns) __syncthreads();
   if (norm) {
     const float* w = a.weight[t];
     auto partner = [&](int e) {
@@ -215,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a)
       } else {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xch[row][e0 + i] = x0[i], xch[row][e1 + i] = x1[i];
+        for (int i = 0; i < 8; ++i) xch[row][xch_at(e0 + i)] = x0[i], xch[row][xch_at(e1 + i)] = x1[i];
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int u = e0 + i, v = e1 + i;
-          y0[i] = xch[row][u >= r ? u : (u < half ? u + half : u - half)];
-          y1[i] = xch[row][v >= r ? v : (v < half ? v + half : v - half)];
+          y0[i] = xch[row][xch_at(u >= r ? u : (u < half ? u + half : u - half))];
+          y1[i] = xch[row][xch_at(v >= r ? v : (v < half ? v + half : v - half))];
         }
       }
 #pragma unroll
@@ -244,15 +268,24 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const RotaryArgs a)
   }
 }
 
+template <class Tin, class Tout, int kMode>
+cudaError_t go(const RotaryArgs& a, dim3 grid, cudaStream_t st) {
+  auto* kernel = rotary_kernel<Tin, Tout, kMode>;
+  constexpr int bytes = rotary_smem<Tin, kMode>();
+  static std::atomic<bool> done[64];
+  cudaError_t e = once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kThreads, bytes, st>>>(a);
+  return cudaGetLastError();
+}
+
 template <class Tin, class Tout>
 cudaError_t launch(const RotaryArgs& a, dim3 grid, cudaStream_t st) {
-  if (a.interleaved)
-    rotary_kernel<Tin, Tout, kInterleaved><<<grid, kThreads, 0, st>>>(a);
-  else if (a.r % 16 == 0)
-    rotary_kernel<Tin, Tout, kHalfPaired><<<grid, kThreads, 0, st>>>(a);
-  else
-    rotary_kernel<Tin, Tout, kHalfAny><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  if (a.interleaved) return go<Tin, Tout, kInterleaved>(a, grid, st);
+  if (a.r % 16 == 0) return go<Tin, Tout, kHalfPaired>(a, grid, st);
+  return go<Tin, Tout, kHalfAny>(a, grid, st);
 }
 
 }  // namespace
