@@ -62,6 +62,12 @@ __device__ __forceinline__ void put8(__nv_bfloat16* p, const float x[8]) {
                                             pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 __device__ __forceinline__ void put8(float* p, const float x[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // a whole sector in one store
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+    return;
+  }
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
