@@ -22,7 +22,8 @@
  *     pb = prefix / 128 dense-prefix blocks, nbv = nb - pb video blocks,
  *     k_eff = min(top_k, nbv).
  *   - Every pointer argument is a DEVICE pointer owned by the caller, except
- *     in bsa_forward_host, whose h* arguments are HOST pointers.  The library
+ *     in bsa_forward_host, whose h* arguments are HOST pointers, and
+ *     bsa_rotary_freqs, which works on the host alone.  The library
  *     allocates no memory and keeps no per-call state.
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Calls are asynchronous on that stream: a return of BSA_OK
