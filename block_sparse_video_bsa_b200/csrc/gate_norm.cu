@@ -442,11 +442,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
       }
     }
   }
+  const int group = threadIdx.x / s.threads;
+  RowReduce* red = reinterpret_cast<RowReduce*>(sm + s.off_red) + group;
+  if (threadIdx.x % s.threads == 0) red->no[0] = red->no[1] = 0;
   asm volatile("bar.sync 0, %0;" ::"r"(rows_threads) : "memory");   // the producer is on its way
 
-  const int group = threadIdx.x / s.threads;
-  RowGroup g{static_cast<int>(threadIdx.x) - group * s.threads, s.threads, 1 + group,
-             reinterpret_cast<RowReduce*>(sm + s.off_red) + group, 0};
+  RowGroup g{static_cast<int>(threadIdx.x) - group * s.threads, s.threads, 1 + group, red,
+             0, 0};
+  int mark = 0;
   // chunks past the row's end read its last one again and neither count nor store
   int at[CH];
   bool in[CH];
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     // own last row, so its phase is the current one at most), then that this one
     // has landed.  The whole group goes on or none of it.
     const bool read = round == 0 || mbar_wait(&ctl->empty[st], (round - 1) & 1, wc);
-    if (!g.all(read && mbar_wait(&ctl->full[st], round & 1, wc))) break;
+    if (!g.all(read && mbar_wait(&ctl->full[st], round & 1, wc), mark)) break;
     const uint8_t* stage = sm + s.off_stage + st * s.stage_bytes;
     uint64_t* empty = &ctl->empty[st];
     const Tx* xs = reinterpret_cast<const Tx*>(stage + sub * s.x_bytes);

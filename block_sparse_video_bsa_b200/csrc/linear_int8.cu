@@ -261,11 +261,12 @@ cudaError_t go_few(const LinearInt8Args& a, const CUtensorMap& mw, const CUtenso
 // half of TMEM.
 constexpr int kPairThreads = 320;    // warps 0-7 epilogue, 8 producer, 9 MMA
 constexpr int kPairRows = 256;
+constexpr int kTable = 128;          // columns of an epilogue warp
 
 template <int kN>
 struct PairSmem {
   static constexpr uint32_t kA = 128 * kSlice, kB = kN / 2 * kSlice;
-  static constexpr uint32_t kStaging = 8 * 32 * 33 * 4;     // a 32 x 32 block a warp
+  static constexpr uint32_t kStaging = 8 * 32 * 33 * 4;     // a 32 x 32 block, or the table, a warp
   static constexpr int kRing = static_cast<int>((227 * 1024 - 1024 - 512 - kStaging) / (kA + kB));
   static constexpr uint32_t kOffStaging = kRing * (kA + kB);
   static constexpr uint32_t kCtl = kOffStaging + kStaging;
@@ -286,16 +287,17 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&w)[8]) {
 
 // 32 output values of row `row`, columns col .. col + 31, from int32 sums: one
 // row a thread, whole 32-byte sectors.
+// scales, biases: of these columns, in shared memory.
 __device__ __forceinline__ void finish_row(const LinearInt8Args& a, int64_t row, int col, float rs,
-                                           const uint32_t (&v)[32]) {
+                                           const uint32_t (&v)[32], const float* scales,
+                                           const float* biases) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     float o[16];
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-      const float4 cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col + 16 * q + j));
-      float4 cb = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.bias) cb = __ldg(reinterpret_cast<const float4*>(a.bias + col + 16 * q + j));
+      const float4 cs = *reinterpret_cast<const float4*>(scales + 16 * q + j);
+      const float4 cb = *reinterpret_cast<const float4*>(biases + 16 * q + j);
       const int at = 16 * q + j;
       const float2 p0 = mul2(make_float2(static_cast<int32_t>(v[at]), static_cast<int32_t>(v[at + 1])),
                              make_float2(rs, rs));
@@ -445,6 +447,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row = static_cast<int64_t>(r) * kPairRows + rank * 128 + quad * 32 + lane;
       const bool row_ok = row < a.M;
       const float rs = row_ok ? __ldg(a.a_scale + row) : 0.f;
+      if (wide) {
+        // this warp's columns' scales and biases, on their way while the tile accumulates
+        float* tab = reinterpret_cast<float*>(stage);
+        const int col = c * kN + side * (kN / 2) + 4 * lane;
+        if (4 * lane < kN / 2) {
+          float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), cb = cs;
+          if (col + 4 <= a.N) {
+            cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col));
+            if (a.bias) cb = __ldg(reinterpret_cast<const float4*>(a.bias + col));
+          }
+          reinterpret_cast<float4*>(tab)[lane] = cs;
+          reinterpret_cast<float4*>(tab + kTable)[lane] = cb;
+        }
+        __syncwarp();
+      }
       if (!mbar_wait(&ctl->acc_full[buf], (it >> 1) & 1, wc)) break;
       __syncwarp();
       tc_fence_after();
@@ -456,9 +473,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         tmem_wait_ld();
         const int col = c * kN + c0;
         if (wide && col + 32 <= a.N) {
-          if (row_ok) finish_row(a, row, col, rs, v);
+          const float* tab = reinterpret_cast<const float*>(stage) + c0 - side * (kN / 2);
+          if (row_ok) finish_row(a, row, col, rs, v, tab, tab + kTable);
           __syncwarp();
         } else if (col < a.N) {
+          // a cut block behind whole ones: the table has served
+          __syncwarp();
           finish_block(a, row - lane, col, rs, v, stage);
         }
       }

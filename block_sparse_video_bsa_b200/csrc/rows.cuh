@@ -28,6 +28,7 @@ constexpr float kInt8Floor = 0x1p-100f;
 // written again every thread has passed the barrier of the reduction between.
 struct RowReduce {
   float4 part[2][32];
+  int no[4];           // marks of RowGroup::all (two are used), cleared beforehand
 };
 
 // The threads that share a row: a whole CTA, or one of several groups of
@@ -42,19 +43,20 @@ struct RowGroup {
   __device__ __forceinline__ void sync() const {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
   }
-  // True on every thread when it is true on all (one barrier).
-  __device__ __forceinline__ bool all(bool ok) const {
-    if (threads == 32) return __all_sync(0xffffffffu, ok);
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %3, 0;\n\t"
-        "barrier.cta.red.and.pred p, %1, %2, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"(bar), "r"(threads), "r"(static_cast<uint32_t>(ok))
-        : "memory");
-    return r != 0;
+  // True on every thread when it is true on all (one barrier).  A warp that
+  // says no leaves a mark before the barrier that all read after it; marks
+  // alternate, so a thread that is already at the next one does not disturb.
+  // (A barrier with a reduction of its own, taken row after row by warps whose
+  // threads come out of a wait one by one, was seen to let a group fall apart.)
+  __device__ __forceinline__ bool all(bool ok, int& mark) {
+    ok = __all_sync(0xffffffffu, ok);
+    if (threads == 32) return ok;
+    volatile int* no = red->no;
+    if (!ok && (tid & 31) == 0) no[mark] = 1;
+    sync();
+    ok = no[mark] == 0;
+    mark ^= 1;
+    return ok;
   }
 };
 
