@@ -222,6 +222,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// This thread has read its part of a stage.  The next filling comes through the
+// async proxy, which does not wait for reads of the generic one by itself: the
+// fence orders them before the arrival.
+__device__ __forceinline__ void stage_read(uint64_t* empty) {
+  fence_proxy_async_smem();
+  mbar_arrive(empty);
+}
+
 // 8 values as four pairs: the packed fp32 instructions halve the arithmetic,
 // which is what bounds this kernel next to HBM.
 struct Oct {
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[c].p[j] = fma2(x.p[j], pair(a.residual_scale), h[c].p[j]);
       }
-      if (!s.tok_mod) mbar_arrive(empty);
+      if (!s.tok_mod) stage_read(empty);
       if (a.h) {
         Tx* ho = static_cast<Tx*>(a.h) + b * a.h_b + t * a.h_n;
 #pragma unroll
@@ -543,7 +551,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     } else {
 #pragma unroll
       for (int c = 0; c < CH; ++c) smem8(xs + at[c], h[c]);
-      if (!s.tok_mod) mbar_arrive(empty);
+      if (!s.tok_mod) stage_read(empty);
     }
     if (!a.z) continue;
     const float2 mr =
@@ -585,7 +593,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
           for (int j = 0; j < 4; ++j) h[c].p[j] = add2(h[c].p[j], m.p[j]);
         }
       }
-      mbar_arrive(empty);
+      stage_read(empty);
     }
     const int64_t o = b * a.z_b + t * a.z_n;
     if (a.z_type == kTypeBf16) {
