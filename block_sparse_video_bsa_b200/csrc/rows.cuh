@@ -223,11 +223,15 @@ __device__ __forceinline__ float4 row_partials(RowGroup& g, float4 mine) {
   return p;
 }
 
-// Sum over the row's threads.
-__device__ __forceinline__ float row_sum(RowGroup& g, float v) {
+// Mean of n values over the row's threads, the quotient rounded once: the
+// product with 1 / n, then a step with what it leaves (an overflowed sum stays
+// infinite).
+__device__ __forceinline__ float row_mean(RowGroup& g, float v, int n) {
   v = warp_sum(v);
-  if (g.warps() == 1) return v;
-  return warp_sum(row_partials(g, make_float4(v, 0.f, 0.f, 0.f)).x);
+  if (g.warps() > 1) v = warp_sum(row_partials(g, make_float4(v, 0.f, 0.f, 0.f)).x);
+  const float count = static_cast<float>(n), inv = 1.f / count;
+  const float m = v * inv;
+  return m <= 3.402823466e38f ? fmaf(fmaf(-m, count, v), inv, m) : m;
 }
 
 // Largest value over the row's threads; v >= 0 or NaN, and a NaN anywhere wins (as an
@@ -287,8 +291,11 @@ __device__ __forceinline__ float2 row_moments(RowGroup& g, const float (&x)[CH][
 // Code of one value, in the low byte: the product is rounded to fp32, and the
 // sum with 1.5 2^23 rounds it to a whole number, half to even (|product| <=
 // 127.00002), whose two's complement is the sum's low bits.
+__device__ __forceinline__ uint32_t code_of(float product) {
+  return __float_as_uint(__fadd_rn(product, 12582912.f));
+}
 __device__ __forceinline__ uint32_t code_bits(float x, float inv) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.f));
+  return code_of(__fmul_rn(x, inv));
 }
 __device__ __forceinline__ uint32_t codes4(const float* x, float inv) {
   const uint32_t lo = __byte_perm(code_bits(x[0], inv), code_bits(x[1], inv), 0x0040);

@@ -612,3 +612,33 @@ def test_two_streams_at_once(cuda_dev):
     for i in range(2):
         for g in got[i]:
             assert torch.equal(g, want[i])
+
+
+@pytest.mark.parametrize("token", [False, True])
+@pytest.mark.parametrize("B,N,C", [(1, 20_000, 7_168), (2, 700, 2_048), (1, 3_000, 1_111), (1, 1, 7_168), (3, 40, 65)])
+def test_gate_norm_codes_are_those_of_its_rows(cuda_dev, B, N, C, token):
+    # quantised in the same pass or afterwards from fp32: the same codes and scales, to the bit
+    if token and N * C > 10_000_000:
+        N //= 8
+    x = rnd(600, B, N, C, dtype=torch.bfloat16)
+    mod = [0.3 * rnd(601 + i, B, N if token else 1, C) for i in range(2)]
+    for pre in ("rms", "layer"):
+        _, z = bsa.gate_norm(x, None, None, *mod, pre=pre, z_dtype=torch.float32)
+        _, (codes, top) = bsa.gate_norm(x, None, None, *mod, pre=pre, quantize=True)
+        want, scale = bsa.quantize_int8(z.reshape(B * N, C))
+        assert torch.equal(top, scale)
+        assert torch.equal(codes.reshape(B * N, C), want)
+
+
+@pytest.mark.parametrize("N", [2, 1_000])
+def test_gate_norm_sum_of_squares_past_fp32(cuda_dev, N):
+    # the mean square overflows: the factor is 0 and z the shift, but for infinities themselves
+    C = 7_168
+    x = rnd(610, 1, N, C)
+    x[0, 0] = 1e25
+    x[0, 1, 5] = float("inf")
+    shift = rnd(611, 1, 1, C)
+    _, z = bsa.gate_norm(x, shift=shift, pre="rms", z_dtype=torch.float32)
+    assert torch.equal(z[0, 0], shift[0, 0])
+    rest = torch.arange(C, device=z.device) != 5
+    assert torch.equal(z[0, 1, rest], shift[0, 0, rest]) and z[0, 1, 5].isnan()
