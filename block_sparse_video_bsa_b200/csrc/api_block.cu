@@ -16,6 +16,7 @@ using bsa::cuda_status;
 constexpr int kMaxN = 1 << 21;        // tokens a batch entry, as the attention
 constexpr int kMaxGrid = 65535;
 constexpr int kMaxRow = 32768;        // values of a normed or quantised row; K of the product
+constexpr int kMaxSide = 1 << 30;     // rows and columns of the product: tile indices are 32-bit
 
 int type_size(int t) { return t == BSA_DTYPE_BF16 ? 2 : (t == BSA_DTYPE_FP32 ? 4 : 1); }
 bool float_type(int t) { return t == BSA_DTYPE_BF16 || t == BSA_DTYPE_FP32; }
@@ -293,6 +294,7 @@ int linear_int8_entry(const bsa_linear_int8_params* params, const int8_t* a, con
   bsa_linear_int8_params own = *params;
   bsa_linear_int8_params* p = &own;
   if (p->M < 1 || p->N < 1 || p->K < 1 || p->K > kMaxRow) return BSA_ERR_INVALID;
+  if (p->M > kMaxSide || p->N > kMaxSide) return BSA_ERR_INVALID;
   if (!float_type(p->out_dtype)) return BSA_ERR_INVALID;
   if (!a || !a_scale || !w || !w_scale || !out) return BSA_ERR_INVALID;
   // the stride of a single row is never used

@@ -428,11 +428,11 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-// Default semantics (release at CTA scope): what the arrival hands over is TMEM,
-// which the tcgen05 fences order; a release at cluster scope would also wait for
-// this thread's global stores.
+// What the arrival hands over is TMEM, which the tcgen05 fences order; a release
+// would also wait for this thread's global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 // 2-D tile into this CTA's shared memory, counted on a barrier of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map,

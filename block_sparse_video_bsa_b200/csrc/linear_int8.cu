@@ -410,6 +410,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         if (++stage == kRing) stage = 0, ++round;
       }
     }
+    // every issued load has landed before the CTAs exit (rank 0's barriers count both)
+    if (rank == 0) {
+      const int64_t issued = static_cast<int64_t>(round) * kRing + stage;
+      for (int64_t k = issued > kRing ? issued - kRing : 0; k < issued; ++k)
+        mbar_wait(&ctl->full[k % kRing], static_cast<uint32_t>(k / kRing) & 1, wc);
+    }
   } else if (warp == 9 && lane == 0 && rank == 0) {
     const uint32_t id = idesc_s8_s32(kPairRows, kN);
     uint32_t stage = 0, round = 0;

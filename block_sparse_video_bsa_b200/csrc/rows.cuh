@@ -46,8 +46,8 @@ struct RowGroup {
   // True on every thread when it is true on all (one barrier).  A warp that
   // says no leaves a mark before the barrier that all read after it; marks
   // alternate, so a thread that is already at the next one does not disturb.
-  // (A barrier with a reduction of its own, taken row after row by warps whose
-  // threads come out of a wait one by one, was seen to let a group fall apart.)
+  // The vote also brings a warp together whose threads came out of a wait one
+  // by one, before it arrives at a barrier that counts whole warps.
   __device__ __forceinline__ bool all(bool ok, int& mark) {
     ok = __all_sync(0xffffffffu, ok);
     if (threads == 32) return ok;

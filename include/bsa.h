@@ -634,7 +634,8 @@ int bsa_quantize_int8(const bsa_quantize_int8_params* p, const void* x, int8_t* 
                       void* stream);
 
 typedef struct {
-  int32_t M, N, K;           /* tokens, output channels, input channels <= 32768 */
+  int32_t M, N, K;           /* tokens, output channels (2^30 at most), input
+                                channels <= 32768                             */
   int32_t out_dtype;         /* bf16 or fp32                                  */
   int64_t lda, ldw;          /* bytes from row to row, multiples of 16, >= K  */
   int64_t ldo;               /* elements from row to row of out, >= N         */

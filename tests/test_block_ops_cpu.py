@@ -285,3 +285,8 @@ def test_forward_block_workspace():
     assert want <= n <= want + 8 * 256
     bp.C = 0
     assert bsa.lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp)) == 0
+
+
+def test_linear_int8_refuses_sides_past_32_bit_tiles():
+    assert _lin(M=(1 << 30) + 1, K=16, lda=16) == bsa.BSA_ERR_INVALID
+    assert _lin(N=2**31 - 1, K=16, ldw=16, ldo=2**31) == bsa.BSA_ERR_INVALID
