@@ -680,7 +680,8 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
     have another head count than q.  ``out`` gives the outputs (a tensor may be its own output)."""
     outs = out if out is not None else (None, None, None)
     device, want, launches = _rotary_plan(
-        (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions), _sig(freqs),
+        (_sig(q), _sig(k), _sig(v)), outs if out is None else tuple([_sig(y) for y in outs]),
+        _sig(positions), _sig(freqs),
         (_sig(q_weight), _sig(k_weight)), layout,
         None if axis_pairs is None else tuple(axis_pairs), eps, scale, bool(inverse), out_dtype)
     if stream is not None or _device_now() != device:
@@ -744,7 +745,8 @@ def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, re
         DTYPES[mods[0]] if mods else 1, 2 if quantize and want_z else DTYPES[z_dtype], eps,
         residual_scale, branch_scale, *_rows(x, C), *_rows(y, C), *h, N * ld, ld,
         *_mod(gate, B, N, C, where), *_mod(scale, B, N, C, where), *_mod(shift, B, N, C, where))
-    return device, p, ((B, N, C), (N * C, C, 1)), ((B * N, ld), (ld, 1)), C, ld
+    return (device, p, ctypes.byref(p), ((B, N, C), (N * C, C, 1)), ((B * N, C), (ld, 1)),
+            x[2] == (N * C, C, 1))
 
 
 def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weight=None,
@@ -757,7 +759,7 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     x, y [B, N, C]; gate, scale, shift [C], [B, C], [B, 1, C] or [B, N, C]; weights and biases fp32
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
-    device, p, shape, codes, C, ld = _gate_norm_plan(
+    device, p, ref, shape, codes, packed = _gate_norm_plan(
         _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
         (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out), pre,
         post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z)
@@ -770,9 +772,10 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         _need(dev_status.get_device() == device, "gate_norm")
         p = bsa_gate_norm_params.from_buffer_copy(p)
         p.dev_status = dev_status.data_ptr()
+        ref = ctypes.byref(p)
     h, z, zs = h_out, None, None
     if h is None and y is not None:
-        h = _new(shape[0], shape[1], dtype=x.dtype, device=x.device)
+        h = torch.empty_like(x) if packed else _new(shape[0], shape[1], dtype=x.dtype, device=x.device)
     if want_z and quantize:
         z = _new(codes[0], codes[1], dtype=torch.int8, device=x.device)
         zs = _new(codes[0][:1], (1,), dtype=torch.float32, device=x.device)
@@ -780,13 +783,13 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         z = _new(shape[0], shape[1], dtype=z_dtype, device=x.device)
     i = bsa_gate_norm_inputs(*[None if t is None else t.data_ptr() for t in (
         x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias)])
-    rc = lib().bsa_gate_norm(ctypes.byref(p), ctypes.byref(i), None if h is None else h.data_ptr(),
+    rc = lib().bsa_gate_norm(ref, ctypes.byref(i), None if h is None else h.data_ptr(),
                              None if z is None else z.data_ptr(),
                              None if zs is None else zs.data_ptr(), _raw_stream(device))
     if rc:
         raise BsaError(rc, "bsa_gate_norm")
     if zs is not None:
-        z = (z if ld == C else z[:, :C], zs)
+        z = z, zs
     return (x if h is None else h), z
 
 
@@ -816,11 +819,11 @@ def quantize_int8(x, stream=None):
     if not _here(device, stream):
         with _elsewhere(device, stream, "quantize_int8"):
             return quantize_int8(x)
-    codes = _new((rows, ld), (ld, 1), dtype=torch.int8, device=x.device)
+    codes = _new((rows, K), (ld, 1), dtype=torch.int8, device=x.device)
     scale = _new((rows,), (1,), dtype=torch.float32, device=x.device)
     _check(lib().bsa_quantize_int8(p, x.data_ptr(), codes.data_ptr(), scale.data_ptr(),
                                    _raw_stream(device)), "bsa_quantize_int8")
-    return (codes if ld == K else codes[:, :K]), scale
+    return codes, scale
 
 
 @functools.lru_cache(maxsize=256)
@@ -838,25 +841,29 @@ def _linear_int8_plan(a, a_scale, w, w_scale, bias, out, out_dtype):
         out_dtype = out[0]
         _need(out[1] == (M, N) and (N == 1 or out[2][1] == 1), where)
     _need(out_dtype in _FLOATS, where)
-    return device, (M, N, K, DTYPES[out_dtype], a[2][0], w[2][0], N if out is None else out[2][0])
+    p = bsa_linear_int8_params(M, N, K, DTYPES[out_dtype], a[2][0], w[2][0],
+                               N if out is None else out[2][0])
+    return device, p, ctypes.byref(p), (M, N), (N, 1)
 
 
 def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=None,
                 dev_status=None, stream=None):
     """bsa_linear_int8: a_scale[:, None] * w_scale * (a @ w.T) + bias from int8 codes a [M, K] and
     w [N, K] (rows on 16 bytes, as ``quantize_int8`` lays them out), exact sums, fp32 or bf16 out."""
-    device, p = _linear_int8_plan(_sig(a), _sig(a_scale), _sig(w), _sig(w_scale), _sig(bias),
-                                  _sig(out), out_dtype)
+    device, p, ref, shape, strides = _linear_int8_plan(_sig(a), _sig(a_scale), _sig(w), _sig(w_scale), _sig(bias),
+                                                     _sig(out), out_dtype)
     if not _here(device, stream):
         with _elsewhere(device, stream, "linear_int8"):
             return linear_int8(a, a_scale, w, w_scale, bias, out_dtype, out, dev_status)
-    _need(dev_status is None or dev_status.get_device() == device, "linear_int8")
-    o = out
-    if o is None:
-        o = _new(p[:2], (p[1], 1), dtype=out_dtype, device=a.device)
-    _check(lib().bsa_linear_int8(ctypes.byref(bsa_linear_int8_params(*p, _addr(dev_status))),
-                                 a.data_ptr(), a_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                                 _addr(bias), o.data_ptr(), _raw_stream(device)), "bsa_linear_int8")
+    if dev_status is not None:
+        _need(dev_status.get_device() == device, "linear_int8")
+        p = bsa_linear_int8_params.from_buffer_copy(p)
+        p.dev_status = dev_status.data_ptr()
+        ref = ctypes.byref(p)
+    o = _new(shape, strides, dtype=out_dtype, device=a.device) if out is None else out
+    _check(lib().bsa_linear_int8(ref, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
+                                 w_scale.data_ptr(), None if bias is None else bias.data_ptr(),
+                                 o.data_ptr(), _raw_stream(device)), "bsa_linear_int8")
     return o
 
 
