@@ -324,30 +324,31 @@ __device__ __forceinline__ void finish_row(const LinearInt8Args& a, int64_t row,
   }
 }
 
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 // A warp's block of 32 rows (lane: row row0 + lane, its 32 sums in v) and
 // columns col .. col + 31 where rows start anywhere or the block is cut off:
 // through shared memory, so that a row is written by neighbouring lanes.
 __device__ __forceinline__ void finish_block(const LinearInt8Args& a, int64_t row0, int col,
-                                             float rs, const uint32_t (&v)[32], int32_t* stage) {
+                                             float rs, const uint32_t (&v)[32], float* stage) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = static_cast<int32_t>(v[j]);
+  for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = static_cast<float>(static_cast<int32_t>(v[j])) * rs;
   __syncwarp();
   const bool in = col + lane < a.N;
   const float cs = in ? __ldg(a.w_scale + col + lane) : 0.f;
   const float cb = in && a.bias ? __ldg(a.bias + col + lane) : 0.f;
-  const int rows = static_cast<int>(a.M - row0 < 32 ? a.M - row0 : 32);
-  for (int i = 0; i < rows; ++i) {
-    const float s = __shfl_sync(0xffffffffu, rs, i);
-    const float o = fmaf(static_cast<float>(stage[i * 33 + lane]) * s, cs, cb);
-    const int64_t at = (row0 + i) * a.ldo + col + lane;
-    if (in) {
-      if (a.out_fp32)
-        static_cast<float*>(a.out)[at] = o;
-      else
-        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
-    }
-  }
+  const int64_t at = row0 * a.ldo + col + lane;
+  const int rows = in ? static_cast<int>(a.M - row0 < 32 ? a.M - row0 : 32) : 0;
+  auto put = [&](auto* p) {
+#pragma unroll 16
+    for (int i = 0; i < rows; ++i, p += a.ldo) store_out(p, fmaf(stage[i * 33 + lane], cs, cb));
+  };
+  if (a.out_fp32)
+    put(static_cast<float*>(a.out) + at);
+  else
+    put(static_cast<__nv_bfloat16*>(a.out) + at);
   __syncwarp();
 }
 
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp < 8) {
     // warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31, a half of the columns each
     const int quad = warp & 3, side = warp >> 2;
-    int32_t* stage = reinterpret_cast<int32_t*>(sm + S::kOffStaging) + warp * 32 * 33;
+    float* stage = reinterpret_cast<float*>(sm + S::kOffStaging) + warp * 32 * 33;
     int it = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++it) {
       const int buf = it & 1;
@@ -455,7 +456,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       const float rs = row_ok ? __ldg(a.a_scale + row) : 0.f;
       if (wide) {
         // this warp's columns' scales and biases, on their way while the tile accumulates
-        float* tab = reinterpret_cast<float*>(stage);
+        float* tab = stage;
         const int col = c * kN + side * (kN / 2) + 4 * lane;
         if (4 * lane < kN / 2) {
           float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), cb = cs;
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         tmem_wait_ld();
         const int col = c * kN + c0;
         if (wide && col + 32 <= a.N) {
-          const float* tab = reinterpret_cast<const float*>(stage) + c0 - side * (kN / 2);
+          const float* tab = stage + c0 - side * (kN / 2);
           if (row_ok) finish_row(a, row, col, rs, v, tab, tab + kTable);
           __syncwarp();
         } else if (col < a.N) {
