@@ -9,7 +9,6 @@ device is not sm_100 the call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import re
@@ -188,6 +187,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        L.addresses = {name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                       for name in _SIGS}
         _lib = L
     return _lib
 
@@ -548,7 +549,34 @@ def bsa_debug_expired_wait(dev_status, timeout_ns: int, stream=None):
 # the host's share small: checks of shapes, strides and types and the filled
 # parameter struct are a pure function of the arguments' layout and are kept
 # per layout (never per address); a repeated layout costs a lookup, the output
-# allocations and the launch.
+# allocations and the launch, which csrc/host.cpp does (norm of one row: 13.5 us
+# a call in Python alone, 8.4 with it).
+
+_host = None
+
+
+def _load_host():
+    """The extension module built from csrc/host.cpp (raises if it was not built)."""
+    global _host
+    if _host is None:
+        if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_host.so")):
+            raise RuntimeError("_host.so is missing: run `python -m "
+                               "block_sparse_video_bsa_b200.build` first")
+        from . import _host as module
+        _host = module
+    return _host
+
+
+def _keep(plans, key, plan):
+    """Remember a layout's plan; a program has a handful of them."""
+    if len(plans) >= 256:
+        plans.clear()
+    plans[key] = plan
+    return plan
+
+
+_rotary_plans, _gate_norm_plans, _quantize_plans, _linear_plans = {}, {}, {}, {}
+
 
 def _need(ok, where):
     if not ok:
@@ -594,8 +622,6 @@ def _addr(t):
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
-# torch.empty's argument handling costs a microsecond more than empty_strided's
-_new = torch.empty_strided
 
 
 def _packed(shape):
@@ -623,7 +649,6 @@ def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_lengt
     return torch.tensor(out, dtype=torch.float64, device=device), scale.value
 
 
-@functools.lru_cache(maxsize=256)
 def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inverse, out_dtype):
     """(device, output shapes and types, launches): a launch is the filled struct and which of q, k
     and v it takes (those that share their layout)."""
@@ -666,7 +691,7 @@ def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inver
                               (_i32 * 4)(*pairs), int(inverse), DTYPES[dtype], DTYPES[odtype],
                               scale, eps, stride[0], stride[1], stride[2], ostride[0], ostride[1],
                               ostride[2], pos_b, pstride[-2])
-        launches.append((ctypes.byref(p), tuple(i in ids for i in range(3))))
+        launches.append((p, ctypes.addressof(p), tuple(i in ids for i in range(3))))
     return device, tuple(want), tuple(launches)
 
 
@@ -679,27 +704,29 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
     freqs fp64 [pairs] from ``rotary_freqs``; axis_pairs lists the pairs of each axis.  k and v may
     have another head count than q.  ``out`` gives the outputs (a tensor may be its own output)."""
     outs = out if out is not None else (None, None, None)
-    device, want, launches = _rotary_plan(
-        (_sig(q), _sig(k), _sig(v)), outs if out is None else tuple([_sig(y) for y in outs]),
-        _sig(positions), _sig(freqs),
-        (_sig(q_weight), _sig(k_weight)), layout,
-        None if axis_pairs is None else tuple(axis_pairs), eps, scale, bool(inverse), out_dtype)
+    if axis_pairs is not None:
+        axis_pairs = tuple(axis_pairs)
+    host = _host or _load_host()
+    key = (host.layout(q, k, v, *outs, positions, freqs, q_weight, k_weight), layout, axis_pairs,
+           eps, scale, inverse, out_dtype)
+    plan = _rotary_plans.get(key)
+    if plan is None:
+        plan = _keep(_rotary_plans, key, _rotary_plan(
+            (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions),
+            _sig(freqs), (_sig(q_weight), _sig(k_weight)), layout, axis_pairs, eps, scale,
+            bool(inverse), out_dtype))
+    device, want, launches = plan
     if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "rotary"):
             return rotary(q, k, v, positions, freqs, layout, axis_pairs, q_weight, k_weight, eps,
                           scale, inverse, out, out_dtype)
-    where = freqs.device
-    Q, K, V = [y if w is None or y is not None else _new(w[0], w[1], dtype=w[2], device=where)
+    Q, K, V = [y if w is None or y is not None else host.empty(*w, freqs)
                for w, y in zip(want, outs)]
-    call, st = lib().bsa_rotary, _raw_stream(device)
-    at, fr = positions.data_ptr(), freqs.data_ptr()
-    for p, (i, j, k_) in launches:
-        rc = call(p, q.data_ptr() if i else None, k.data_ptr() if j else None,
-                  v.data_ptr() if k_ else None, at, fr,
-                  q_weight.data_ptr() if i and q_weight is not None else None,
-                  k_weight.data_ptr() if j and k_weight is not None else None,
-                  Q.data_ptr() if i else None, K.data_ptr() if j else None,
-                  V.data_ptr() if k_ else None, st)
+    at, st = lib().addresses["bsa_rotary"], _raw_stream(device)
+    for _, p, (i, j, k_) in launches:
+        rc = host.call(at, p, q if i else None, k if j else None, v if k_ else None, positions,
+                       freqs, q_weight if i else None, k_weight if j else None, Q if i else None,
+                       K if j else None, V if k_ else None, st)
         if rc:
             raise BsaError(rc, "bsa_rotary")
     return Q, K, V
@@ -723,7 +750,6 @@ def _rows(g, C):
     return (0, 0) if g is None else (g[2][0], g[2][1])
 
 
-@functools.lru_cache(maxsize=256)
 def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, residual_scale,
                     branch_scale, quantize, z_dtype, want_z):
     where = "gate_norm"
@@ -745,8 +771,8 @@ def _gate_norm_plan(x, y, gate, scale, shift, vectors, h_out, pre, post, eps, re
         DTYPES[mods[0]] if mods else 1, 2 if quantize and want_z else DTYPES[z_dtype], eps,
         residual_scale, branch_scale, *_rows(x, C), *_rows(y, C), *h, N * ld, ld,
         *_mod(gate, B, N, C, where), *_mod(scale, B, N, C, where), *_mod(shift, B, N, C, where))
-    return (device, p, ctypes.byref(p), ((B, N, C), (N * C, C, 1)), ((B * N, C), (ld, 1)),
-            x[2] == (N * C, C, 1))
+    return (device, p, ctypes.addressof(p), ((B, N, C), (N * C, C, 1)), ((B * N, C), (ld, 1)),
+            ((B * N,), (1,)))
 
 
 def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weight=None,
@@ -759,10 +785,17 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     x, y [B, N, C]; gate, scale, shift [C], [B, C], [B, 1, C] or [B, N, C]; weights and biases fp32
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
-    device, p, ref, shape, codes, packed = _gate_norm_plan(
-        _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
-        (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out), pre,
-        post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z)
+    host = _host or _load_host()
+    key = (host.layout(x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias,
+                       h_out), pre, post, eps, residual_scale, branch_scale, quantize, z_dtype,
+           want_z)
+    plan = _gate_norm_plans.get(key)
+    if plan is None:
+        plan = _keep(_gate_norm_plans, key, _gate_norm_plan(
+            _sig(x), _sig(y), _sig(gate), _sig(scale), _sig(shift),
+            (_sig(post_weight), _sig(post_bias), _sig(pre_weight), _sig(pre_bias)), _sig(h_out),
+            pre, post, eps, residual_scale, branch_scale, quantize, z_dtype, want_z))
+    device, p, ref, rows, codes, scales = plan
     if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "gate_norm"):
             return gate_norm(x, y, gate, scale, shift, pre, pre_weight, pre_bias, post, post_weight,
@@ -772,28 +805,22 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
         _need(dev_status.get_device() == device, "gate_norm")
         p = bsa_gate_norm_params.from_buffer_copy(p)
         p.dev_status = dev_status.data_ptr()
-        ref = ctypes.byref(p)
+        ref = ctypes.addressof(p)
     h, z, zs = h_out, None, None
     if h is None and y is not None:
-        h = torch.empty_like(x) if packed else _new(shape[0], shape[1], dtype=x.dtype, device=x.device)
+        h = host.empty(*rows, x.dtype, x)
     if want_z and quantize:
-        z = _new(codes[0], codes[1], dtype=torch.int8, device=x.device)
-        zs = _new(codes[0][:1], (1,), dtype=torch.float32, device=x.device)
+        z, zs = host.empty(*codes, torch.int8, x), host.empty(*scales, torch.float32, x)
     elif want_z:
-        z = _new(shape[0], shape[1], dtype=z_dtype, device=x.device)
-    i = bsa_gate_norm_inputs(*[None if t is None else t.data_ptr() for t in (
-        x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias)])
-    rc = lib().bsa_gate_norm(ref, ctypes.byref(i), None if h is None else h.data_ptr(),
-                             None if z is None else z.data_ptr(),
-                             None if zs is None else zs.data_ptr(), _raw_stream(device))
+        z = host.empty(*rows, z_dtype, x)
+    rc = host.call(lib().addresses["bsa_gate_norm"], ref,
+                   (x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias), h, z,
+                   zs, _raw_stream(device))
     if rc:
         raise BsaError(rc, "bsa_gate_norm")
-    if zs is not None:
-        z = z, zs
-    return (x if h is None else h), z
+    return (x if h is None else h), (z if zs is None else (z, zs))
 
 
-@functools.lru_cache(maxsize=256)
 def _quantize_int8_plan(x):
     where = "quantize_int8"
     device = _one_device(where, x)
@@ -808,25 +835,28 @@ def _quantize_int8_plan(x):
     K = S * L
     ld = -(-K // 16) * 16
     p = bsa_quantize_int8_params(B, N, S, L, DTYPES[dtype], *s, ld)
-    return device, ctypes.byref(p), B * N, K, ld
+    return device, p, ctypes.addressof(p), ((B * N, K), (ld, 1)), ((B * N,), (1,))
 
 
 def quantize_int8(x, stream=None):
     """bsa_quantize_int8: (codes, scales) of the rows of x [M, K] or [B, N, K], or of the token rows
     of an attention output [B, H, N, D] (H D values a token).  codes int8 [rows, K] (row stride a
     multiple of 16), scales fp32 [rows]."""
-    device, p, rows, K, ld = _quantize_int8_plan(_sig(x))
+    host = _host or _load_host()
+    key = host.layout(x)
+    plan = _quantize_plans.get(key)
+    if plan is None:
+        plan = _keep(_quantize_plans, key, _quantize_int8_plan(_sig(x)))
+    device, _, p, rows, scales = plan
     if not _here(device, stream):
         with _elsewhere(device, stream, "quantize_int8"):
             return quantize_int8(x)
-    codes = _new((rows, K), (ld, 1), dtype=torch.int8, device=x.device)
-    scale = _new((rows,), (1,), dtype=torch.float32, device=x.device)
-    _check(lib().bsa_quantize_int8(p, x.data_ptr(), codes.data_ptr(), scale.data_ptr(),
-                                   _raw_stream(device)), "bsa_quantize_int8")
+    codes, scale = host.empty(*rows, torch.int8, x), host.empty(*scales, torch.float32, x)
+    _check(host.call(lib().addresses["bsa_quantize_int8"], p, x, codes, scale,
+                     _raw_stream(device)), "bsa_quantize_int8")
     return codes, scale
 
 
-@functools.lru_cache(maxsize=256)
 def _linear_int8_plan(a, a_scale, w, w_scale, bias, out, out_dtype):
     where = "linear_int8"
     device = _one_device(where, a, a_scale, w, w_scale, bias, out)
@@ -843,15 +873,20 @@ def _linear_int8_plan(a, a_scale, w, w_scale, bias, out, out_dtype):
     _need(out_dtype in _FLOATS, where)
     p = bsa_linear_int8_params(M, N, K, DTYPES[out_dtype], a[2][0], w[2][0],
                                N if out is None else out[2][0])
-    return device, p, ctypes.byref(p), (M, N), (N, 1)
+    return device, p, ctypes.addressof(p), ((M, N), (N, 1))
 
 
 def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out=None,
                 dev_status=None, stream=None):
     """bsa_linear_int8: a_scale[:, None] * w_scale * (a @ w.T) + bias from int8 codes a [M, K] and
     w [N, K] (rows on 16 bytes, as ``quantize_int8`` lays them out), exact sums, fp32 or bf16 out."""
-    device, p, ref, shape, strides = _linear_int8_plan(_sig(a), _sig(a_scale), _sig(w), _sig(w_scale), _sig(bias),
-                                                     _sig(out), out_dtype)
+    host = _host or _load_host()
+    key = (host.layout(a, a_scale, w, w_scale, bias, out), out_dtype)
+    plan = _linear_plans.get(key)
+    if plan is None:
+        plan = _keep(_linear_plans, key, _linear_int8_plan(
+            _sig(a), _sig(a_scale), _sig(w), _sig(w_scale), _sig(bias), _sig(out), out_dtype))
+    device, p, ref, rows = plan
     if not _here(device, stream):
         with _elsewhere(device, stream, "linear_int8"):
             return linear_int8(a, a_scale, w, w_scale, bias, out_dtype, out, dev_status)
@@ -859,11 +894,10 @@ def linear_int8(a, a_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, out
         _need(dev_status.get_device() == device, "linear_int8")
         p = bsa_linear_int8_params.from_buffer_copy(p)
         p.dev_status = dev_status.data_ptr()
-        ref = ctypes.byref(p)
-    o = _new(shape, strides, dtype=out_dtype, device=a.device) if out is None else out
-    _check(lib().bsa_linear_int8(ref, a.data_ptr(), a_scale.data_ptr(), w.data_ptr(),
-                                 w_scale.data_ptr(), None if bias is None else bias.data_ptr(),
-                                 o.data_ptr(), _raw_stream(device)), "bsa_linear_int8")
+        ref = ctypes.addressof(p)
+    o = host.empty(*rows, out_dtype, a) if out is None else out
+    _check(host.call(lib().addresses["bsa_linear_int8"], ref, a, a_scale, w, w_scale, bias, o,
+                     _raw_stream(device)), "bsa_linear_int8")
     return o
 
 

@@ -1,4 +1,5 @@
-"""Build libbsa.so in-tree with nvcc for sm_100a (cross-compiles without a GPU).
+"""Build libbsa.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and _host.so, the
+host part of the Python wrappers, with g++.
 
 Usage:  python -m block_sparse_video_bsa_b200.build   (or __graft_entry__.build())
 """
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsa.so")
+HOST = os.path.join(PKG, "_host.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["api.cu", "pool_summarize.cu", "select.cu", "attend.cu", "attend_fp8.cu", "quant_fp8.cu",
            "reblock.cu", "extra.cu", "noalloc.cu", "api_block.cu", "rotary.cu", "gate_norm.cu",
@@ -44,6 +46,19 @@ def _newer(target: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def _host_command(source: str) -> list:
+    import sysconfig
+
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(os.path.dirname(lib), "include"),
+            "-I", os.path.join(os.path.dirname(lib), "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], source,
+            "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", "-o", HOST]
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -58,18 +73,22 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if force or not _newer(o, [s] + headers):
             jobs.append([nvcc, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    source = os.path.join(CSRC, "host.cpp")
+    if force or not _newer(HOST, [source]):
+        jobs.append(_host_command(source))
+
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr, flush=True)
 
     with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
         list(ex.map(run, jobs))
-    if force or jobs or not _newer(LIB, objs):
+    if force or not _newer(LIB, objs):
         run([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", LIB])
     return LIB
 

@@ -290,3 +290,31 @@ def test_forward_block_workspace():
 def test_linear_int8_refuses_sides_past_32_bit_tiles():
     assert _lin(M=(1 << 30) + 1, K=16, lda=16) == bsa.BSA_ERR_INVALID
     assert _lin(N=2**31 - 1, K=16, ldw=16, ldo=2**31) == bsa.BSA_ERR_INVALID
+
+
+def test_layout_keys_tell_layouts_apart():
+    layout = bsa._load_host().layout
+    x = torch.zeros(4, 6, 8)
+    same = torch.ones(4, 6, 8)
+    assert layout(x, None) == layout(same, None)                    # never the address or the values
+    others = [(x,), (None, x), (x, x), (x.bfloat16(), None), (x.int(), None), (x.transpose(0, 1), None), (x[:2], None), (x[..., :4], None),
+              (x.reshape(24, 8), None), (x[0], None), (x[:, :1].expand(4, 6, 8), None), (x.to("meta"), None)]
+    keys = [layout(*t) for t in others] + [layout(x, None)]
+    assert len(set(keys)) == len(keys)
+    with pytest.raises(TypeError):
+        layout(x, 3)
+
+
+def test_host_outputs_and_calls_check_their_arguments():
+    host, x = bsa._load_host(), torch.zeros(3)
+    y = host.empty((2, 5), (16, 1), torch.int8, x)
+    assert y.shape == (2, 5) and y.stride() == (16, 1) and y.dtype is torch.int8 and y.device == x.device
+    for bad in (lambda: host.empty((2,), (1, 1), torch.int8, x), lambda: host.empty((-1,), (1,), torch.int8, x),
+                lambda: host.empty((1,), (1,), "int8", x), lambda: host.empty((1,) * 9, (1,) * 9, torch.int8, x),
+                lambda: host.call(), lambda: host.call(0), lambda: host.call(1, "x"), lambda: host.call(1, *range(13)),
+                lambda: host.call(1, (None,) * 17)):
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            bad()
+    at = bsa.lib().addresses
+    assert host.call(at["bsa_quantize_int8"], None, x, x, x, None) == bsa.BSA_ERR_INVALID
+    assert host.call(at["bsa_gate_norm"], None, (x, None), x, None, None, None) == bsa.BSA_ERR_INVALID
