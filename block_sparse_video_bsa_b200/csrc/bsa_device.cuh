@@ -408,6 +408,15 @@ __device__ __forceinline__ void mma_s8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// Programmatic launches: a kernel launched so may be resident while the one
+// before it in the stream still runs; grid_wait returns when that one is done and
+// its writes are seen, and nothing in global memory is touched before.
+// grid_ready lets the next one come.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_ready() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- CTA pairs (clusters of two): one MMA over both CTAs' shared memory ----
 // CTA rank 0 issues; its A rows are D rows 0-127, the peer's are 128-255, and
 // each holds one half of B's rows.  D's rows stay in the TMEM of their CTA.

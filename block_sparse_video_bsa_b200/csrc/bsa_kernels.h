@@ -26,6 +26,30 @@ cudaError_t once_per_device(std::atomic<bool> (&done)[64], F set) {
   return e;
 }
 
+// A launch that may start while the kernel before it in the stream still runs
+// (it waits for that one on the device: grid_wait in bsa_device.cuh).  cluster:
+// CTAs a cluster where the kernel does not say so itself.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                         int cluster, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next call
+  return e;
+}
+
 struct Shape {
   int B, H, N;      // D is fixed at 128
   int nb;           // ceil(N / 128)

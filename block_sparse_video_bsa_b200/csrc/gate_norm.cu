@@ -104,6 +104,8 @@ __device__ __forceinline__ void store_z8(const RowGroup& g, const GateNormArgs& 
 
 template <class Tx, int CH, int kThreads, int kBlocks, int kMode>
 __global__ void __launch_bounds__(kThreads, kBlocks) gate_norm_kernel(const GateNormArgs a) {
+  grid_wait();
+  grid_ready();
   __shared__ RowReduce red;
   RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
@@ -359,6 +361,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
     fence_barrier_init();
   }
   __syncthreads();
+  grid_wait();
+  grid_ready();
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
   // the CTA's rows in turn: s.rows neighbours of every gridDim.x-th block of them
   const int blocks = (a.N + s.rows - 1) / s.rows;
@@ -702,8 +706,7 @@ cudaError_t launch_ring_ch(const GateNormArgs& a, const RingShape& s, dim3 grid,
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
   });
   if (e != cudaSuccess) return e;
-  kernel<<<grid, s.groups * s.threads + 32, s.bytes, st>>>(a, s);
-  return cudaGetLastError();
+  return launch_early(kernel, grid, s.groups * s.threads + 32, s.bytes, st, 0, a, s);
 }
 
 template <class Tx, class Ty>
@@ -717,8 +720,7 @@ cudaError_t launch_ring(const GateNormArgs& a, const RingShape& s, int ch, dim3 
 template <class Tx, int kMode>
 cudaError_t launch(const GateNormArgs& a, int ch, int threads, int blocks, cudaStream_t st) {
   auto go = [&](auto k) {
-    k<<<blocks, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k, dim3(blocks), threads, 0, st, 0, a);
   };
   if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, 1, kMode>);
   if (ch == 2) return threads <= 512 ? go(gate_norm_kernel<Tx, 2, 512, 2, kMode>)

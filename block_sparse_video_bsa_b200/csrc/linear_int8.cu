@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_wait();
+  grid_ready();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
 
@@ -233,20 +235,7 @@ cudaError_t go_few(const LinearInt8Args& a, const CUtensorMap& mw, const CUtenso
   if (e != cudaSuccess) return e;
   const int rt = (a.N + kRowTile - 1) / kRowTile;
   const int split = few_split(rt, (a.K + kSlice - 1) / kSlice);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split * rt);
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, mw, ma, a, split);
-  if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next call
-  return e;
+  return launch_early(kernel, dim3(split * rt), kFewThreads, S::kBytes, st, split, mw, ma, a, split);
 }
 
 // ------------------------------------------------------------ CTA pairs
@@ -385,6 +374,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  grid_wait();
+  grid_ready();
   const uint32_t tmem = ctl->tmem_base;
   const WaitCtx wc{&ctl->abort_flag, a.dev_status};
 
@@ -530,8 +521,8 @@ cudaError_t go_pair(const LinearInt8Args& a, const CUtensorMap& ma, const CUtens
   const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.ldo * size % 32 == 0 &&
                     reinterpret_cast<uintptr_t>(a.w_scale) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  kernel<<<2 * pairs, kPairThreads, S::kBytes, st>>>(ma, mw, a, rt, ct, wide);
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(2 * pairs), kPairThreads, S::kBytes, st, 0, ma, mw, a, rt, ct,
+                      static_cast<int>(wide));
 }
 
 }  // namespace

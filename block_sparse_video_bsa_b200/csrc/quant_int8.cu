@@ -16,6 +16,8 @@ namespace {
 // Any rows, fp32 in registers.
 template <class Tx, int CH, int kMode>
 __global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args a) {
+  grid_wait();
+  grid_ready();
   __shared__ RowReduce red;
   RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
@@ -46,6 +48,8 @@ __global__ void __launch_bounds__(1024, 1) quant_int8_kernel(const QuantInt8Args
 // is taken on them as 16-bit integers, which order magnitudes with NaN on top.
 template <int CH, int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(const QuantInt8Args a) {
+  grid_wait();
+  grid_ready();
   __shared__ RowReduce red;
   RowGroup g{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), 0, &red, 0, 0};
   const int64_t rows = static_cast<int64_t>(a.B) * a.N;
@@ -94,8 +98,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(cons
 template <class Tx, int kMode>
 cudaError_t launch(const QuantInt8Args& a, int ch, int threads, int blocks, cudaStream_t st) {
   auto go = [&](auto k) {
-    k<<<blocks, threads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_early(k, dim3(blocks), threads, 0, st, 0, a);
   };
   if (ch == 1) return go(quant_int8_kernel<Tx, 1, kMode>);
   if (ch == 2) return go(quant_int8_kernel<Tx, 2, kMode>);
@@ -120,8 +123,7 @@ cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cud
       if (resident > 0 && blocks > 148 * resident) blocks = 148 * resident;
     }
     auto go = [&](auto k) {
-      k<<<blocks, threads, 0, st>>>(a);
-      return cudaGetLastError();
+      return launch_early(k, dim3(blocks), threads, 0, st, 0, a);
     };
     if (ch == 1) return go(quant_int8_bf16_kernel<1, 1024, 1>);
     if (threads <= 256) return go(quant_int8_bf16_kernel<4, 256, 6>);

@@ -125,6 +125,8 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a)
     }
     cp_async_commit();
   };
+  grid_wait();
+  grid_ready();
 #pragma unroll
   for (int j = 0; j < kDepth - 1; ++j) fetch(j);
 
@@ -283,8 +285,7 @@ cudaError_t go(const RotaryArgs& a, dim3 grid, cudaStream_t st) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, bytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(kernel, grid, kThreads, bytes, st, 0, a);
 }
 
 template <class Tin, class Tout>

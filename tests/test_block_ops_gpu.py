@@ -642,3 +642,50 @@ def test_gate_norm_sum_of_squares_past_fp32(cuda_dev, N):
     assert torch.equal(z[0, 0], shift[0, 0])
     rest = torch.arange(C, device=z.device) != 5
     assert torch.equal(z[0, 1, rest], shift[0, 0, rest]) and z[0, 1, 5].isnan()
+
+
+@pytest.mark.parametrize("M,C,H", [(1, 512, 2), (1, 7_168, 56), (40, 1_111, 3), (300, 512, 4), (5_000, 640, 2)])
+def test_calls_in_a_row_see_each_other(cuda_dev, M, C, H):
+    # launches overlap their starts with the call before: every value a call reads is written by that one or by the caller, again and
+    # again into the same places, and nothing may be read early or written over late
+    x0 = rnd(700, 1, M, C)
+    w1, s1 = bsa.quantize_int8(rnd(701, 3 * H * 128, C))
+    w2, s2 = bsa.quantize_int8(rnd(702, C, H * 128))
+    pos = torch.arange(M, dtype=torch.int32, device=x0.device)
+    freqs, _ = bsa.rotary_freqs(64)
+    qkv = torch.empty(M, 3 * H * 128, dtype=torch.bfloat16, device=x0.device)
+    heads = torch.empty(1, H, M, 128, dtype=torch.bfloat16, device=x0.device)
+    y = torch.empty(M, C, dtype=torch.bfloat16, device=x0.device)
+
+    def chain(x, wait):
+        for _ in range(6):
+            _, (a, sa) = bsa.gate_norm(x, pre="rms", quantize=True)
+            wait()
+            bsa.linear_int8(a, sa, w1, s1, out=qkv)
+            wait()
+            q = qkv.view(1, M, 3, H, 128)[:, :, 0].transpose(1, 2)
+            bsa.rotary(q, None, None, pos, freqs, out=(heads, None, None))
+            wait()
+            a, sa = bsa.quantize_int8(heads)
+            wait()
+            bsa.linear_int8(a, sa, w2, s2, out=y)
+            wait()
+            bsa.gate_norm(x, y[None], post="rms", h_out=x, want_z=False)
+            wait()
+            x.mul_(0.5)
+            wait()
+        return x
+
+    want = chain(x0.clone(), torch.cuda.synchronize)
+    for _ in range(10):
+        assert torch.equal(chain(x0.clone(), lambda: None), want)
+    x = x0.clone()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream), torch.cuda.graph(graph, stream=stream):
+        chain(x, lambda: None)
+    for _ in range(3):
+        x.copy_(x0)
+        graph.replay()
+        assert torch.equal(x, want)
