@@ -348,6 +348,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                             int row_tiles, int col_tiles, int wide) {
   using S = PairSmem<kN>;
   constexpr int kRing = S::kRing;
+  constexpr int kBuf = kN > 128 ? 256 : 128;      // TMEM columns of a tile's sums
+  constexpr int kSide = (kN / 32 + 1) / 2 * 32;   // columns of warps 0-3; the rest are warps 4-7's
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   PairCtl* ctl = reinterpret_cast<PairCtl*>(sm + S::kCtl);
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, 2 * kN);
+  if (warp == 9) tmem_alloc_pair(&ctl->tmem_base, kN > 128 ? 512 : 256);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t ra = smem_u32(sm + stage * (S::kA + S::kB));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_s8_ss_pair(tmem + buf * kN, smem_desc_sw128(ra + kk * 32, 16, 1024),
+          mma_s8_ss_pair(tmem + buf * kBuf, smem_desc_sw128(ra + kk * 32, 16, 1024),
                          smem_desc_sw128(ra + S::kA + kk * 32, 16, 1024), id, (k | kk) ? 1u : 0u);
         mma_commit_pair(&ctl->empty[stage]);
         if (++stage == kRing) stage = 0, ++round;
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (ok) mma_commit_pair(&ctl->acc_full[buf]);
     }
   } else if (warp < 8) {
-    // warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31, a half of the columns each
+    // warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31, some of the columns each
     const int quad = warp & 3, side = warp >> 2;
     float* stage = reinterpret_cast<float*>(sm + S::kOffStaging) + warp * 32 * 33;
     int it = 0;
@@ -448,8 +450,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (wide) {
         // this warp's columns' scales and biases, on their way while the tile accumulates
         float* tab = stage;
-        const int col = c * kN + side * (kN / 2) + 4 * lane;
-        if (4 * lane < kN / 2) {
+        const int col = c * kN + side * kSide + 4 * lane;
+        if (4 * lane < kSide) {
           float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), cb = cs;
           if (col + 4 <= a.N) {
             cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col));
@@ -463,15 +465,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       if (!mbar_wait(&ctl->acc_full[buf], (it >> 1) & 1, wc)) break;
       __syncwarp();
       tc_fence_after();
-      const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kN;
+      const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBuf;
 #pragma unroll 1
-      for (int c0 = side * (kN / 2); c0 < (side + 1) * (kN / 2); c0 += 32) {
+      for (int c0 = side * kSide; c0 < (side ? kN : kSide); c0 += 32) {
         uint32_t v[32];
         BSA_TMEM_LD_32(src + c0, v);
         tmem_wait_ld();
         const int col = c * kN + c0;
         if (wide && col + 32 <= a.N) {
-          const float* tab = stage + c0 - side * (kN / 2);
+          const float* tab = stage + c0 - side * kSide;
           if (row_ok) finish_row(a, row, col, rs, v, tab, tab + kTable);
           __syncwarp();
         } else if (col < a.N) {
@@ -491,16 +493,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
   tc_fence_after();
   if (warp == 9) {
     __syncwarp();
-    tmem_dealloc_pair(tmem, 2 * kN);
+    tmem_dealloc_pair(tmem, kN > 128 ? 512 : 256);
   }
 }
 
-// Channels a tile.  128 halve the work of a tile but not its A operand, so they
-// pay only where all tiles run at once (256 x 7,168 x 7,168: 21.2 us against
-// 26.0 with 256; 512 rows, in two waves: 38.0 against 28.7; 2,048: 126 and 88).
+// Channels a tile: those whose waves of 74 pairs cost least, a tile's cost going
+// with the rows that an SM reads for it, 128 + channels / 2 (measured within a
+// tenth over 16 shapes).  256 for many tiles (37,740 x 7,168 x 7,168: 1,233 us
+// against 1,294 with 224); fewer where that fills the last wave (512 x 7,168 x
+// 21,504: 57.7 with 224 and 60.0; 512 x 7,168 x 7,168: 21.2 and 23.9; 128 x
+// 7,168 x 21,504: 34.3 with 160 and 42.9; 256 x 7,168 x 7,168: 18.7 with 128 and
+// 21.6).
 int linear_pair_cols(int M, int N) {
-  const int64_t tiles = static_cast<int64_t>((M + kPairRows - 1) / kPairRows) * ((N + 127) / 128);
-  return tiles <= 74 ? 128 : 256;
+  const int64_t rows = (M + kPairRows - 1) / kPairRows;
+  int best = 256;
+  int64_t least = INT64_MAX;
+  for (int cols = 256; cols >= 128; cols -= 32) {
+    const int64_t waves = (rows * ((N + cols - 1) / cols) + 73) / 74;
+    const int64_t cost = waves * (128 + cols / 2);
+    if (cost < least) best = cols, least = cost;
+  }
+  return best;
 }
 
 template <int kN>
@@ -542,8 +555,13 @@ cudaError_t launch_linear_int8(const LinearInt8Args& a, const CUtensorMap& ma,
   if (a.M <= 16) return go_few<16>(a, mw, ma, st);
   if (a.M <= 32) return go_few<32>(a, mw, ma, st);
   if (a.M <= kFewTokens) return go_few<64>(a, mw, ma, st);
-  return linear_pair_cols(a.M, a.N) == 256 ? go_pair<256>(a, ma, mw, st)
-                                                : go_pair<128>(a, ma, mw, st);
+  switch (linear_pair_cols(a.M, a.N)) {
+    case 128: return go_pair<128>(a, ma, mw, st);
+    case 160: return go_pair<160>(a, ma, mw, st);
+    case 192: return go_pair<192>(a, ma, mw, st);
+    case 224: return go_pair<224>(a, ma, mw, st);
+    default: return go_pair<256>(a, ma, mw, st);
+  }
 }
 
 }  // namespace bsa

@@ -689,3 +689,20 @@ def test_calls_in_a_row_see_each_other(cuda_dev, M, C, H):
         x.copy_(x0)
         graph.replay()
         assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,N", [(512, 256, 7_168), (2_048, 128, 7_168), (100, 144, 10_001), (128, 640, 11_840), (70, 17, 13_016), (300, 256, 7_000),
+                                   (130, 1_000, 13_999), (256, 130, 9_472), (600, 96, 16_000)])
+def test_linear_int8_tiles_of_every_width(cuda_dev, M, K, N, out):
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    ld = -(-K // 16) * 16
+    a, w = [torch.randint(-127, 128, (r, ld), generator=g, device="cuda", dtype=torch.int8)[:, :K] for r in (M, N)]
+    sa, sw = [torch.rand(r, generator=g, device="cuda") + 0.1 for r in (M, N)]
+    bias = torch.randn(N, generator=g, device="cuda")
+    got = bsa.linear_int8(a, sa, w, sw, bias=bias, out_dtype=out).double()
+    scaled = (a.double() @ w.double().T) * sa.double()[:, None] * sw.double()
+    want = scaled + bias.double()
+    # the sum (exact below 2^24), its product with a_scale, the fused step and the last rounding: half a step each
+    room = 2.0**-23 * scaled.abs() + 2.0**-24 * want.abs() + torch.finfo(out).eps / 2 * (want.abs() + 2.0**-22 * scaled.abs()) + 1e-30
+    assert ((got - want).abs() <= room).all()
