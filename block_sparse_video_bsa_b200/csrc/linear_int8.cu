@@ -244,7 +244,7 @@ cudaError_t go_few(const LinearInt8Args& a, const CUtensorMap& mw, const CUtenso
 // x 32: each brings its 128 tokens and half of the channels, so an SM reads
 // 128 + kN / 2 rows for 128 x kN products instead of 128 + kN (one CTA of 128 x
 // 128 took 3,650 us for 37,740 x 7,168 x 7,168, where shared-memory bandwidth
-// bounds it; pairs of 256 x 256 take 1,256 to 1,347 us, 2.9 to 3.1 POP/s with
+// bounds it; pairs of 256 x 256 take 1,190 to 1,430 us, 2.7 to 3.3 POP/s with
 // the clock under the power cap).  Persistent: warp 8 loads, warp 9 of CTA 0
 // issues, warps 0-7 finish a tile while the next accumulates into the other
 // half of TMEM.

@@ -513,7 +513,9 @@ int bsa_forward_extra(const bsa_params* p, int32_t n_extra, const void* Q, const
  * rounded once, to nearest even.  Outputs do not overlap inputs or each other
  * except where an entry says that it works in place (an overlap of the large
  * operands is BSA_ERR_INVALID).  Calls are deterministic, keep no state and
- * can be captured into CUDA graphs. */
+ * can be captured into CUDA graphs.  A call's kernel may become resident while
+ * the kernel before it on the stream still runs; it touches no memory before
+ * that one is done. */
 
 typedef enum {
   BSA_DTYPE_BF16 = 0,
