@@ -559,7 +559,7 @@ def _load_host():
     """The extension module built from csrc/host.cpp (raises if it was not built)."""
     global _host
     if _host is None:
-        if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_host.so")):
+        if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_host.so")):
             raise RuntimeError("_host.so is missing: run `python -m "
                                "block_sparse_video_bsa_b200.build` first")
         from . import _host as module
