@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 import re
 
@@ -704,8 +705,11 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
     freqs fp64 [pairs] from ``rotary_freqs``; axis_pairs lists the pairs of each axis.  k and v may
     have another head count than q.  ``out`` gives the outputs (a tensor may be its own output)."""
     outs = out if out is not None else (None, None, None)
+    # plain numbers: a key that held the caller's object (a tensor of no dimension) would
+    # match by identity and keep its first value
+    eps, scale, inverse = float(eps), float(scale), bool(inverse)
     if axis_pairs is not None:
-        axis_pairs = tuple(axis_pairs)
+        axis_pairs = tuple([operator.index(n) for n in axis_pairs])
     host = _host or _load_host()
     key = (host.layout(q, k, v, *outs, positions, freqs, q_weight, k_weight), layout, axis_pairs,
            eps, scale, inverse, out_dtype)
@@ -714,7 +718,7 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
         plan = _keep(_rotary_plans, key, _rotary_plan(
             (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions),
             _sig(freqs), (_sig(q_weight), _sig(k_weight)), layout, axis_pairs, eps, scale,
-            bool(inverse), out_dtype))
+            inverse, out_dtype))
     device, want, launches = plan
     if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "rotary"):
@@ -786,6 +790,8 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
     host = _host or _load_host()
+    eps, residual_scale, branch_scale = float(eps), float(residual_scale), float(branch_scale)
+    quantize, want_z = bool(quantize), bool(want_z)      # plain values in the key, as in rotary
     key = (host.layout(x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias,
                        h_out), pre, post, eps, residual_scale, branch_scale, quantize, z_dtype,
            want_z)

@@ -318,3 +318,47 @@ def test_host_outputs_and_calls_check_their_arguments():
     at = bsa.lib().addresses
     assert host.call(at["bsa_quantize_int8"], None, x, x, x, None) == bsa.BSA_ERR_INVALID
     assert host.call(at["bsa_gate_norm"], None, (x, None), x, None, None, None) == bsa.BSA_ERR_INVALID
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The wrappers on CPU tensors with the library call replaced: what each call would have passed."""
+    real, seen = bsa._load_host(), []
+
+    class Host:
+        layout, empty = staticmethod(real.layout), staticmethod(real.empty)
+
+        @staticmethod
+        def call(at, params, *args):
+            name = next(n for n, a in bsa.lib().addresses.items() if a == at)
+            kind = bsa._SIGS[name][1][0]._type_
+            seen.append((name, kind.from_buffer_copy(ctypes.string_at(params, ctypes.sizeof(kind))), args))
+            return 0
+    monkeypatch.setattr(bsa, "_host", Host)
+    monkeypatch.setattr(bsa, "_one_device", lambda *a: 0)
+    monkeypatch.setattr(bsa, "_device_now", lambda: 0)
+    monkeypatch.setattr(bsa, "_raw_stream", lambda device: 0)
+    return seen
+
+
+def test_scalars_are_read_at_every_call(launches):
+    # numbers held in tensors of no dimension (a learned layer scale), changed in place between two calls
+    x = torch.zeros(1, 2, 128)
+    s = {n: torch.tensor(0.5) for n in ("eps", "residual_scale", "branch_scale")}
+    q, pos, freqs = torch.zeros(1, 2, 3, 128), torch.zeros(3, dtype=torch.int32), torch.ones(64, dtype=torch.float64)
+    m, inverse, pairs = torch.tensor(0.5), torch.tensor(False), torch.tensor([64])
+    for value in (0.5, 2.0):
+        for t in s.values():
+            t.fill_(value)
+        bsa.gate_norm(x, x, **s)
+        p = launches[-1][1]
+        assert (p.eps, p.residual_scale, p.branch_scale) == (value,) * 3
+        m.fill_(value)
+        inverse.fill_(value > 1)
+        bsa.rotary(q, None, None, pos, freqs, scale=m, eps=m, inverse=inverse, axis_pairs=pairs)
+        p = launches[-1][1]
+        assert (p.scale, p.eps, p.inverse, p.axis_pairs[0]) == (value, value, int(value > 1), 64)
+    want_z = torch.tensor(True)
+    assert bsa.gate_norm(x, x, want_z=want_z)[1] is not None
+    want_z.fill_(False)
+    assert bsa.gate_norm(x, x, want_z=want_z)[1] is None and launches[-1][2][2] is None
