@@ -58,6 +58,50 @@ bool disjoint(int64_t row, int64_t na, int64_t sa, int64_t nb, int64_t sb, int64
   return true;
 }
 
+// Rows of `row` values of `size` bytes at base, three dimensions of them.
+struct Rows {
+  const void* base;
+  int size;
+  int64_t row, n[3], s[3];
+};
+Range range_of(const Rows& r) {
+  return range_of(r.base, r.size, r.row, r.n[0], r.s[0], r.n[1], r.s[1], r.n[2], r.s[2]);
+}
+
+// Some row of `bytes`, `at` bytes past one of the same shape, meets one of these
+// rows: strides in bytes, the largest last, each at least what the smaller ones
+// reach, so of every dimension only the two steps around `at` can come near.
+bool rows_meet(int64_t at, int64_t bytes, const int64_t* n, const int64_t* s, int dims) {
+  if (dims == 0) return at < bytes && -at < bytes;
+  const int64_t step = s[dims - 1], most = n[dims - 1] - 1;
+  if (most == 0) return rows_meet(at, bytes, n, s, dims - 1);
+  const int64_t k0 = at / step - (at % step < 0);
+  for (int64_t k = k0; k <= k0 + 1; ++k)
+    if (k <= most && -k <= most && rows_meet(at - k * step, bytes, n, s, dims - 1)) return true;
+  return false;
+}
+
+// No byte belongs to both: their ranges lie apart, or they are rows of one shape
+// that interleave (views of one buffer).
+bool apart(const Rows& a, const Rows& b) {
+  const Range ra = range_of(a), rb = range_of(b);
+  if (!meet(ra, rb)) return true;
+  bool same = a.size == b.size && a.row == b.row;
+  for (int i = 0; i < 3; ++i)
+    same = same && a.n[i] == b.n[i] && (a.n[i] == 1 || a.s[i] == b.s[i]);
+  if (!same || !disjoint(a.row, a.n[0], a.s[0], a.n[1], a.s[1], a.n[2], a.s[2])) return false;
+  int64_t n[3], s[3];
+  int order[3] = {0, 1, 2};
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (a.s[order[j]] < a.s[order[i]]) {
+        const int t = order[i];
+        order[i] = order[j], order[j] = t;
+      }
+  for (int i = 0; i < 3; ++i) n[i] = a.n[order[i]], s[i] = a.s[order[i]] * a.size;
+  return !rows_meet(static_cast<int64_t>(rb.lo - ra.lo), a.row * a.size, n, s, 3);
+}
+
 // Each entry checks its arguments and, with `launch`, enqueues its kernel: a
 // path of several calls checks all of them before the first launch.
 
@@ -113,16 +157,18 @@ int rotary_entry(const bsa_rotary_params* params, const void* q, const void* k, 
   if (a.ntens == 0) return BSA_ERR_INVALID;
   if (p->rotary_dim > 0 && (q || k) && (!positions || !freqs)) return BSA_ERR_INVALID;
   // Outputs: on their own input exactly, or apart from every input and output.
-  for (int i = 0; i < a.ntens; ++i) {
-    const bool in_place = a.out[i] == a.in[i] && same;
-    const Range ro = range_of(a.out[i], so, 128, p->B, p->out_b, p->H, p->out_h, p->N, p->out_n);
+  auto ins = [&](int i) {
+    return Rows{a.in[i], si, 128, {p->B, p->H, p->N}, {p->in_b, p->in_h, p->in_n}};
+  };
+  auto outs = [&](int i) {
+    return Rows{a.out[i], so, 128, {p->B, p->H, p->N}, {p->out_b, p->out_h, p->out_n}};
+  };
+  for (int i = 0; i < a.ntens; ++i)
     for (int j = 0; j < a.ntens; ++j) {
-      if (j != i && a.out[i] == a.out[j]) return BSA_ERR_INVALID;
-      if (in_place) continue;
-      const Range ri = range_of(a.in[j], si, 128, p->B, p->in_b, p->H, p->in_h, p->N, p->in_n);
-      if (meet(ro, ri)) return BSA_ERR_INVALID;
+      const bool in_place = i == j && a.out[i] == a.in[i] && same;
+      if (!in_place && !apart(outs(i), ins(j))) return BSA_ERR_INVALID;
+      if (j > i && !apart(outs(i), outs(j))) return BSA_ERR_INVALID;
     }
-  }
   for (int i = 0; i < a.ntens; ++i)
     if (!aligned(a.in[i], 16) || !aligned(a.out[i], 16) ||
         (a.weight[i] && !aligned(a.weight[i], 16)))

@@ -362,3 +362,61 @@ def test_scalars_are_read_at_every_call(launches):
     assert bsa.gate_norm(x, x, want_z=want_z)[1] is not None
     want_z.fill_(False)
     assert bsa.gate_norm(x, x, want_z=want_z)[1] is None and launches[-1][2][2] is None
+
+
+# A call that passes every check goes on to the device; without one it reports BSA_ERR_CUDA there.
+checks_alone = pytest.mark.skipif(torch.cuda.is_available(), reason="pretend addresses would be launched on")
+
+
+def _packed(**kw):
+    """Views of one buffer of rows [N, groups, H, 128], in and out."""
+    return dict(dict(in_b=0, in_h=128, in_n=7 * 512, out_b=0, out_h=128, out_n=7 * 512), **kw)
+
+
+def test_rotary_in_place_refuses_rows_that_another_tensor_reads():
+    inv, step = bsa.BSA_ERR_INVALID, 1024          # bytes of a group's rows of 4 heads
+    q, k, v, K, V = A, A + step, A + 2 * step, A + 4 * BIG, A + 5 * BIG
+    at = lambda **p: _rot(dict(dict(q=q, k=k, v=v, Q=q, K=k, V=v), **p), **_packed())  # noqa: E731
+    assert at(k=q, K=K) == inv          # one input twice, turned in place once
+    assert at(v=k, V=V) == inv          # k and v tied
+    assert at(k=q + 256, K=K) == inv    # k starts at q's second head
+    assert at(v=q + 7 * step, V=V) == inv        # at q's second token
+    assert at(v=q + 7 * step * 98 + 768, V=V) == inv
+    assert at(V=k) == inv and at(K=K, V=K + 768) == inv
+
+
+def test_rotary_outputs_do_not_overlap():
+    inv, Q = bsa.BSA_ERR_INVALID, A + 3 * BIG
+    for off in (256, 1024, 100 * 256, 3 * 100 * 256, 4 * 100 * 256 - 256):
+        assert _rot(dict(K=Q + off)) == inv and _rot(dict(V=Q + off)) == inv
+        assert _rot(dict(K=Q - off)) == inv
+
+
+@checks_alone
+def test_rotary_takes_rows_that_interleave():
+    ok, step = bsa.BSA_ERR_CUDA, 1024
+    at = lambda **p: _rot(dict(dict(q=A, k=A + step, v=A + 2 * step), **p), **_packed())  # noqa: E731
+    assert at(Q=A, K=A + step, V=A + 2 * step) == ok                               # in place
+    assert at(Q=A + 3 * step, K=A + 4 * step, V=A + 5 * step) == ok                # beside its inputs
+    assert at(k=A, v=A, Q=A + 3 * step, K=A + 4 * step, V=A + 5 * step) == ok      # one input read three times
+    assert _rot(dict(K=A + 3 * BIG + 4 * 100 * 256)) == ok                         # Q and K one after the other
+
+
+@checks_alone
+def test_rotary_overlap_check_against_every_row():
+    # in place q, k at any offset with the same strides: refused exactly where two rows share a byte
+    g, met = np.random.default_rng(3), 0
+    for _ in range(400):
+        n = [int(g.integers(1, 4)) for _ in range(3)]
+        order, s, reach = g.permutation(3), [0, 0, 0], 128
+        for i in order:
+            s[i] = reach + 8 * int(g.integers(0, 40))
+            reach += (n[i] - 1) * s[i]
+        rows = np.array([2 * (b * s[0] + h * s[1] + t * s[2]) for b in range(n[0]) for h in range(n[1]) for t in range(n[2])])
+        off = 16 * int(g.integers(-reach // 8 - 2, reach // 8 + 3))
+        want = bool((np.abs(rows[:, None] - rows[None] - off) < 256).any())
+        st = dict(in_b=s[0], in_h=s[1], in_n=s[2], out_b=s[0], out_h=s[1], out_n=s[2])
+        got = _rot(dict(q=A, Q=A, k=A + off, K=A + 4 * BIG, v=None, V=None), B=n[0], H=n[1], N=n[2], **st)
+        assert got == (bsa.BSA_ERR_INVALID if want else bsa.BSA_ERR_CUDA), (n, s, off)
+        met += want
+    assert 0 < met < 400      # both kinds were drawn
