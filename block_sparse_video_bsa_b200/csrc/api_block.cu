@@ -229,14 +229,27 @@ int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inpu
   if (h && !disjoint(p->C, p->B, p->h_b, p->N, p->h_n)) return BSA_ERR_INVALID;
   if (z && !disjoint(p->C, p->B, p->z_b, p->N, p->z_n)) return BSA_ERR_INVALID;
   // h may be x itself (the residual updated in place); any other overlap of an
-  // output is refused.
-  const Range rx = range_of(in->x, sx, p->C, p->B, p->x_b, p->N, p->x_n);
-  const Range ry = in->y ? range_of(in->y, sy, p->C, p->B, p->y_b, p->N, p->y_n) : Range{0, 0};
-  const Range rh = h ? range_of(h, sx, p->C, p->B, p->h_b, p->N, p->h_n) : Range{0, 0};
-  const Range rz = z ? range_of(z, sz, p->C, p->B, p->z_b, p->N, p->z_n) : Range{0, 0};
+  // output is refused, with the vectors too: one a token is as large as the rows,
+  // and is read after other rows were written.
+  auto rows = [&](const void* base, int size, int64_t sb, int64_t sn) {
+    return Rows{base, size, p->C, {p->B, p->N, 1}, {sb, sn, 0}};
+  };
+  const Rows x = rows(in->x, sx, p->x_b, p->x_n), y = rows(in->y, sy, p->y_b, p->y_n);
+  const Rows ho = rows(h, sx, p->h_b, p->h_n), zo = rows(z, sz, p->z_b, p->z_n);
+  const Rows vectors[7] = {rows(in->gate, sm, p->gate_b, p->gate_n),
+                           rows(in->scale, sm, p->scale_b, p->scale_n),
+                           rows(in->shift, sm, p->shift_b, p->shift_n),
+                           rows(in->post_weight, 4, 0, 0), rows(in->post_bias, 4, 0, 0),
+                           rows(in->pre_weight, 4, 0, 0), rows(in->pre_bias, 4, 0, 0)};
   const bool in_place = h == in->x && p->h_b == p->x_b && p->h_n == p->x_n;
-  if (h && ((!in_place && meet(rh, rx)) || meet(rh, ry) || meet(rh, rz))) return BSA_ERR_INVALID;
-  if (z && (meet(rz, rx) || meet(rz, ry))) return BSA_ERR_INVALID;
+  if (h && z && !apart(ho, zo)) return BSA_ERR_INVALID;
+  for (const Rows& o : {ho, zo}) {
+    if (!o.base) continue;
+    if (!(o.base == h && in_place) && !apart(o, x)) return BSA_ERR_INVALID;
+    if (in->y && !apart(o, y)) return BSA_ERR_INVALID;
+    for (const Rows& v : vectors)
+      if (v.base && !apart(o, v)) return BSA_ERR_INVALID;
+  }
   if (!aligned(in->x, sx) || (in->y && !aligned(in->y, sy)) || (h && !aligned(h, sx)) ||
       (z && !aligned(z, sz)) || (z_scale && !aligned(z_scale, 4)))
     return BSA_ERR_ALIGN;

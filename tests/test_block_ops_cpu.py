@@ -420,3 +420,28 @@ def test_rotary_overlap_check_against_every_row():
         assert got == (bsa.BSA_ERR_INVALID if want else bsa.BSA_ERR_CUDA), (n, s, off)
         met += want
     assert 0 < met < 400      # both kinds were drawn
+
+
+@pytest.mark.parametrize("name", ["gate", "scale", "shift", "pre_weight", "pre_bias", "post_weight", "post_bias"])
+def test_gate_norm_outputs_over_a_vector(name):
+    inv, h, z = bsa.BSA_ERR_INVALID, A + 2 * BIG, A + 3 * BIG
+    per = dict(gate_b=2560, gate_n=256, scale_b=2560, scale_n=256, shift_b=2560, shift_n=256)
+    for out in (h, z):
+        for kw in ({}, per):                                     # one vector a batch entry, one a token
+            assert _gn({name: out}, **kw) == inv
+            assert _gn({name: out + 2 * 19 * 256}, **kw) == inv      # from the last row on
+    if name in ("gate", "scale", "shift"):
+        assert _gn({name: h}, mod_dtype=0, **per) == inv             # of the rows' own type and strides
+        assert _gn({name: z - 4 * 5000}, **per) == inv               # ends inside z
+
+
+@checks_alone
+def test_gate_norm_takes_rows_that_interleave():
+    wide = dict({n + "_b": 8 * 2560 for n in "xyhz"}, **{n + "_n": 8 * 256 for n in "xyhz"})
+    mods = {f"{n}_{d}": 8 * (2560 if d == "b" else 256) for n in ("gate", "scale", "shift") for d in "bn"}
+    part = [A + 512 * i for i in range(8)]
+    inp = dict(x=part[0], y=part[1], gate=part[2], scale=part[3], shift=part[4])
+    for h in (part[5], part[0]):                                     # beside the inputs, or in place
+        assert _gn(inp, h=h, z=part[6], mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_CUDA
+    assert _gn(inp, h=part[5], z=part[5], mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_INVALID
+    assert _gn(inp, h=part[5], z=part[5] + 256, mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_INVALID
