@@ -587,6 +587,36 @@ int bsa_forward_block(const bsa_params* p, const bsa_block_params* bp, const bsa
                  reinterpret_cast<uintptr_t>(workspace) + block_carve(p, bp->C, nullptr, nullptr)};
   if (meet(ws, range_of(x, sx, bp->C, rows, bp->C)) || meet(ws, range_of(out, sx, bp->C, rows, bp->C)))
     return BSA_ERR_INVALID;
+  // and it and the result apart from the weights and vectors
+  const int64_t hd = static_cast<int64_t>(p->H) * 128, C = bp->C;
+  const int sm = type_size(bp->mod_dtype);
+  const struct {
+    const void* base;
+    int size;
+    int64_t row, n0, s0, n1, s1;
+  } read[] = {{w->w_qkv, 1, C, 3 * hd, bp->ld_qkv, 1, 0},
+              {w->w_out, 1, hd, C, bp->ld_out, 1, 0},
+              {w->gate, sm, C, p->B, bp->gate_b, p->N, bp->gate_n},
+              {w->scale, sm, C, p->B, bp->scale_b, p->N, bp->scale_n},
+              {w->shift, sm, C, p->B, bp->shift_b, p->N, bp->shift_n},
+              {w->positions, 4, bp->axes, p->B, bp->pos_b, p->N, bp->pos_n},
+              {w->s_qkv, 4, 3 * hd, 1, 0, 1, 0},
+              {w->b_qkv, 4, 3 * hd, 1, 0, 1, 0},
+              {w->s_out, 4, C, 1, 0, 1, 0},
+              {w->b_out, 4, C, 1, 0, 1, 0},
+              {w->pre_weight, 4, C, 1, 0, 1, 0},
+              {w->pre_bias, 4, C, 1, 0, 1, 0},
+              {w->post_weight, 4, C, 1, 0, 1, 0},
+              {w->post_bias, 4, C, 1, 0, 1, 0},
+              {w->q_weight, 4, 128, 1, 0, 1, 0},
+              {w->k_weight, 4, 128, 1, 0, 1, 0},
+              {w->freqs, 8, bp->rotary_dim / 2, 1, 0, 1, 0}};
+  const Range res = range_of(out, sx, bp->C, rows, bp->C);
+  for (const auto& r : read) {
+    if (!r.base) continue;
+    const Range in = range_of(r.base, r.size, r.row, r.n0, r.s0, r.n1, r.s1);
+    if (meet(ws, in) || meet(res, in)) return BSA_ERR_INVALID;
+  }
   BlockWs b;
   block_carve(p, bp->C, static_cast<uint8_t*>(workspace), &b);
   int rc = block_run(p, bp, w, x, out, b, stream, false);

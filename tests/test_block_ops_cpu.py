@@ -445,3 +445,16 @@ def test_gate_norm_takes_rows_that_interleave():
         assert _gn(inp, h=h, z=part[6], mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_CUDA
     assert _gn(inp, h=part[5], z=part[5], mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_INVALID
     assert _gn(inp, h=part[5], z=part[5] + 256, mod_dtype=0, **wide, **mods) == bsa.BSA_ERR_INVALID
+
+
+@pytest.mark.parametrize("name", ["gate", "scale", "shift", "w_qkv", "s_qkv", "b_qkv", "w_out", "s_out", "b_out", "pre_weight", "pre_bias",
+                                  "post_weight", "post_bias", "q_weight", "k_weight", "positions", "freqs"])
+def test_forward_block_workspace_and_result_lie_apart_from_what_is_read(name):
+    inv, ws = bsa.BSA_ERR_INVALID, A + 8 * BIG
+    p, bp = bsa.params(1, 2, 1000, 3), bsa.bsa_block_params(C=256)
+    n = bsa.lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp))
+    for at in (ws, ws + n // 2 // 256 * 256, ws + n - 256, A + BIG, A + BIG + 512 * 999):
+        assert _block(ptr={name: at}) == inv, hex(at)
+    for bases in (dict(), {name: ws + n}):
+        if not torch.cuda.is_available():
+            assert _block(ptr=bases) == bsa.BSA_ERR_CUDA        # every check passed
