@@ -165,6 +165,7 @@ _SIGS["bsa_forward_reblock_host"] = (ctypes.c_int, [_P] + _HOST12)
 _SIGS["bsa_rotary_freqs"] = (ctypes.c_int, [_i32, ctypes.c_double, _i32] + [ctypes.c_double] * 4
                              + [_vp, _vp])
 _SIGS["bsa_rotary"] = (ctypes.c_int, [ctypes.POINTER(bsa_rotary_params)] + [_vp] * 11)
+_SIGS["bsa_rotary_each"] = _SIGS["bsa_rotary"]
 _SIGS["bsa_gate_norm"] = (ctypes.c_int, [ctypes.POINTER(bsa_gate_norm_params),
                                          ctypes.POINTER(bsa_gate_norm_inputs)] + [_vp] * 4)
 _SIGS["bsa_quantize_int8"] = (ctypes.c_int, [ctypes.POINTER(bsa_quantize_int8_params)] + [_vp] * 4)
@@ -651,8 +652,8 @@ def rotary_freqs(pairs, base=10000.0, scaling="plain", factor=1.0, trained_lengt
 
 
 def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inverse, out_dtype):
-    """(device, output shapes and types, launches): a launch is the filled struct and which of q, k
-    and v it takes (those that share their layout)."""
+    """(device, output shapes and types, the filled structs of q, k and v, the address and the entry to
+    call with it): one struct where the given tensors share their layout."""
     where = "rotary"
     given = [g for g in parts if g is not None]
     _need(given and len(outs) == 3 and pos is not None and fr is not None, where)
@@ -686,14 +687,16 @@ def _rotary_plan(parts, outs, pos, fr, weights, layout, pairs, eps, scale, inver
         _need(y[0] in _FLOATS and y[1] == shape and y[2][3] == 1, where)
         want.append((tuple(y[1]), _packed(y[1]), y[0]))
         kinds.setdefault((H, stride, dtype, y[2], y[0]), []).append(i)
-    launches = []
+    each = (bsa_rotary_params * 3)()
     for (H, stride, dtype, ostride, odtype), ids in kinds.items():
-        p = bsa_rotary_params(B, H, N, 128, 2 * fr[1][0], ROPE_LAYOUTS[layout], len(pairs),
-                              (_i32 * 4)(*pairs), int(inverse), DTYPES[dtype], DTYPES[odtype],
-                              scale, eps, stride[0], stride[1], stride[2], ostride[0], ostride[1],
-                              ostride[2], pos_b, pstride[-2])
-        launches.append((p, ctypes.addressof(p), tuple(i in ids for i in range(3))))
-    return device, tuple(want), tuple(launches)
+        for i in ids:
+            each[i] = bsa_rotary_params(B, H, N, 128, 2 * fr[1][0], ROPE_LAYOUTS[layout],
+                                        len(pairs), (_i32 * 4)(*pairs), int(inverse), DTYPES[dtype],
+                                        DTYPES[odtype], scale, eps, *stride[:3], *ostride[:3], pos_b,
+                                        pstride[-2])
+    if len(kinds) > 1:
+        return device, tuple(want), each, ctypes.addressof(each), "bsa_rotary_each"
+    return device, tuple(want), each, ctypes.addressof(each[i]), "bsa_rotary"
 
 
 def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=None, k_weight=None,
@@ -719,20 +722,17 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
             (_sig(q), _sig(k), _sig(v)), tuple([_sig(y) for y in outs]), _sig(positions),
             _sig(freqs), (_sig(q_weight), _sig(k_weight)), layout, axis_pairs, eps, scale,
             inverse, out_dtype))
-    device, want, launches = plan
+    device, want, _, p, name = plan
     if stream is not None or _device_now() != device:
         with _elsewhere(device, stream, "rotary"):
             return rotary(q, k, v, positions, freqs, layout, axis_pairs, q_weight, k_weight, eps,
                           scale, inverse, out, out_dtype)
     Q, K, V = [y if w is None or y is not None else host.empty(*w, freqs)
                for w, y in zip(want, outs)]
-    at, st = lib().addresses["bsa_rotary"], _raw_stream(device)
-    for _, p, (i, j, k_) in launches:
-        rc = host.call(at, p, q if i else None, k if j else None, v if k_ else None, positions,
-                       freqs, q_weight if i else None, k_weight if j else None, Q if i else None,
-                       K if j else None, V if k_ else None, st)
-        if rc:
-            raise BsaError(rc, "bsa_rotary")
+    rc = host.call(lib().addresses[name], p, q, k, v, positions, freqs, q_weight, k_weight, Q, K, V,
+                   _raw_stream(device))
+    if rc:
+        raise BsaError(rc, name)
     return Q, K, V
 
 

@@ -196,6 +196,69 @@ int rotary_entry(const bsa_rotary_params* params, const void* q, const void* k, 
                                         static_cast<cudaStream_t>(stream)));
 }
 
+// q, k and v with parameters of their own: every check before the first launch,
+// then one launch for each set of tensors that lie alike.
+int rotary_each_entry(const bsa_rotary_params* p, const void* const (&in)[3],
+                      const int32_t* positions, const double* freqs, const float* const (&weight)[3],
+                      void* const (&out)[3], void* stream) {
+  if (!p) return BSA_ERR_INVALID;
+  int first = -1, set[3];
+  auto rows = [&](int i, bool input) {
+    const bsa_rotary_params& r = p[i];
+    const int size = type_size(input ? r.in_dtype : r.out_dtype);
+    if (input) return Rows{in[i], size, 128, {r.B, r.H, r.N}, {r.in_b, r.in_h, r.in_n}};
+    return Rows{out[i], size, 128, {r.B, r.H, r.N}, {r.out_b, r.out_h, r.out_n}};
+  };
+  auto alike = [](const Rows& a, const Rows& b) {
+    bool same = a.size == b.size;
+    for (int d = 0; d < 3; ++d)
+      same = same && a.n[d] == b.n[d] && (a.n[d] == 1 || a.s[d] == b.s[d]);
+    return same;
+  };
+  // the tensors `from` and on of set `s` (all where s is negative), as bsa_rotary takes them
+  auto run = [&](int from, int s, bool launch) {
+    const void* x[3] = {};
+    void* y[3] = {};
+    const float* w[3] = {};
+    for (int i = from; i < (s < 0 ? from + 1 : 3); ++i)
+      if (s < 0 || (in[i] && set[i] == s)) x[i] = in[i], y[i] = out[i], w[i] = weight[i];
+    return rotary_entry(p + from, x[0], x[1], x[2], positions, freqs, w[0], w[1], y[0], y[1], y[2],
+                        stream, launch);
+  };
+  for (int i = 0; i < 3; ++i) {
+    if (!in[i] && !out[i] && !weight[i]) continue;
+    const int rc = run(i, -1, false);
+    if (rc) return rc;
+    if (first < 0) first = i;
+    const bsa_rotary_params &a = p[first], &b = p[i];
+    bool one = a.B == b.B && a.N == b.N && a.rotary_dim == b.rotary_dim && a.layout == b.layout &&
+               a.axes == b.axes && !a.inverse == !b.inverse && a.scale == b.scale &&
+               a.eps == b.eps && (a.B == 1 || a.pos_b == b.pos_b) && (a.N == 1 || a.pos_n == b.pos_n);
+    for (int d = 0; one && d < a.axes; ++d) one = a.axis_pairs[d] == b.axis_pairs[d];
+    if (!one) return BSA_ERR_INVALID;
+    set[i] = i;
+    for (int j = first; j < i; ++j)
+      if (in[j] && set[i] == i && alike(rows(i, true), rows(j, true)) &&
+          alike(rows(i, false), rows(j, false)))
+        set[i] = set[j];
+  }
+  if (first < 0) return BSA_ERR_INVALID;
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j) {
+      if (!in[i] || !in[j]) continue;
+      const Rows o = rows(i, false), x = rows(j, true);
+      const bool in_place = i == j && o.base == x.base && alike(o, x);
+      if (!in_place && !apart(o, x)) return BSA_ERR_INVALID;
+      if (j > i && !apart(o, rows(j, false))) return BSA_ERR_INVALID;
+    }
+  for (int i = first; i < 3; ++i) {
+    if (!in[i] || set[i] != i) continue;
+    const int rc = run(i, i, true);
+    if (rc) return rc;
+  }
+  return BSA_OK;
+}
+
 // ------------------------------------------------------------------ gate norm
 
 int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,
@@ -551,6 +614,15 @@ int bsa_rotary(const bsa_rotary_params* params, const void* q, const void* k, co
                const int32_t* positions, const double* freqs, const float* q_weight,
                const float* k_weight, void* Q, void* K, void* V, void* stream) {
   return rotary_entry(params, q, k, v, positions, freqs, q_weight, k_weight, Q, K, V, stream, true);
+}
+
+int bsa_rotary_each(const bsa_rotary_params* params, const void* q, const void* k, const void* v,
+                    const int32_t* positions, const double* freqs, const float* q_weight,
+                    const float* k_weight, void* Q, void* K, void* V, void* stream) {
+  const void* const in[3] = {q, k, v};
+  void* const out[3] = {Q, K, V};
+  const float* const weight[3] = {q_weight, k_weight, nullptr};
+  return rotary_each_entry(params, in, positions, freqs, weight, out, stream);
 }
 
 int bsa_gate_norm(const bsa_gate_norm_params* params, const bsa_gate_norm_inputs* in, void* h, void* z,

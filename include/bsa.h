@@ -579,6 +579,16 @@ int bsa_rotary(const bsa_rotary_params* p, const void* q, const void* k, const v
                const int32_t* positions, const double* freqs, const float* q_weight,
                const float* k_weight, void* Q, void* K, void* V, void* stream);
 
+/* bsa_rotary where q, k and v have head counts, strides or types of their own:
+ * p[0] is q's, p[1] k's and p[2] v's (not looked at for a tensor that is NULL).
+ * B, N and what says how rows turn (rotary_dim to axis_pairs, inverse, scale,
+ * eps, strides of positions) are the same in all.  Every check, also of one
+ * tensor's output against another's rows, comes before the first launch; tensors
+ * that lie alike share one. */
+int bsa_rotary_each(const bsa_rotary_params p[3], const void* q, const void* k, const void* v,
+                    const int32_t* positions, const double* freqs, const float* q_weight,
+                    const float* k_weight, void* Q, void* K, void* V, void* stream);
+
 typedef enum { BSA_NORM_NONE = 0, BSA_NORM_RMS = 1, BSA_NORM_LAYER = 2 } bsa_norm;
 
 typedef struct {

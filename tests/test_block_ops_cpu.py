@@ -458,3 +458,64 @@ def test_forward_block_workspace_and_result_lie_apart_from_what_is_read(name):
     for bases in (dict(), {name: ws + n}):
         if not torch.cuda.is_available():
             assert _block(ptr=bases) == bsa.BSA_ERR_CUDA        # every check passed
+
+
+def _rot_each(ptrs=None, own=None, **kw):
+    """q with 4 heads, k and v with 2, each in an allocation of its own."""
+    base = dict(B=1, H=4, N=100, D=128, rotary_dim=128, layout=0, axes=1, inverse=0, in_dtype=0, out_dtype=0, scale=1.0, eps=1e-6,
+                in_b=0, in_h=128, in_n=512, out_b=0, out_h=100 * 128, out_n=128, pos_b=0, pos_n=1)
+    s = (bsa.bsa_rotary_params * 3)()
+    for i, n in enumerate("qkv"):
+        p = dict(base, **kw)
+        if i:
+            p.update(H=2, in_n=256)
+        p.update((own or {}).get(n, {}))
+        s[i] = bsa.bsa_rotary_params(**p)
+        s[i].axis_pairs = (ctypes.c_int32 * 4)(64)
+    a = dict(q=A, k=A + BIG, v=A + 2 * BIG, pos=A, freqs=A, qw=None, kw=None, Q=A + 3 * BIG, K=A + 4 * BIG, V=A + 5 * BIG)
+    a.update(ptrs or {})
+    return bsa.lib().bsa_rotary_each(s, *[a[n] for n in ("q", "k", "v", "pos", "freqs", "qw", "kw", "Q", "K", "V")], None)
+
+
+def test_rotary_each_refusals():
+    inv, al = bsa.BSA_ERR_INVALID, bsa.BSA_ERR_ALIGN
+    assert bsa.lib().bsa_rotary_each(None, *[None] * 10, None) == inv
+    assert _rot_each(dict(q=None, k=None, v=None, Q=None, K=None, V=None)) == inv
+    assert _rot_each(dict(q=None, Q=None, qw=A)) == inv and _rot_each(dict(V=None)) == inv and _rot_each(dict(pos=None)) == inv
+    # what one tensor alone would be refused for, in any place
+    for n in "qkv":
+        for bad in (dict(H=0), dict(in_n=-1), dict(out_n=64), dict(in_dtype=2), dict(in_b=1 << 50, B=2)):
+            assert _rot_each(own={n: bad}) == inv, (n, bad)
+        assert _rot_each({n: A + BIG * "qkv".index(n) + 8}) == al and _rot_each({n.upper(): A + BIG * (3 + "qkv".index(n)) + 8}) == al
+        assert _rot_each(own={n: dict(in_n=516)}) == al
+    # parameters of the turn that differ
+    for bad in (dict(N=99), dict(B=2), dict(rotary_dim=126), dict(layout=1), dict(inverse=1), dict(scale=2.0), dict(eps=0.0), dict(pos_n=2)):
+        assert _rot_each(own=dict(v=bad)) == inv, bad
+    # outputs over the rows of a tensor that another launch reads or writes
+    inplace = dict(q=dict(out_h=128, out_n=512))
+    assert _rot_each(dict(Q=A, k=A + 1024, K=A + 4 * BIG), own=inplace) == inv
+    assert _rot_each(dict(Q=A + BIG)) == inv and _rot_each(dict(K=A)) == inv and _rot_each(dict(V=A + 3 * BIG + 4 * 100 * 256 - 256)) == inv
+    assert _rot_each(dict(K=A + 5 * BIG + 256)) == inv
+
+
+@checks_alone
+def test_rotary_each_passes_what_lies_apart():
+    cu = bsa.BSA_ERR_CUDA
+    inplace = dict(q=dict(out_h=128, out_n=512), k=dict(out_h=128, out_n=256), v=dict(out_h=128, out_n=256))
+    assert _rot_each() == cu and _rot_each(dict(qw=A, kw=A)) == cu
+    assert _rot_each(dict(Q=A, K=A + BIG, V=A + 2 * BIG), own=inplace) == cu
+    assert _rot_each(dict(v=A + BIG)) == cu and _rot_each(own=dict(k=dict(pos_b=5))) == cu
+    assert _rot_each(dict(q=None, Q=None)) == cu and _rot_each(own=dict(q=dict(in_dtype=1, in_n=640))) == cu
+
+
+def test_rotary_of_several_layouts_is_one_call(launches):
+    # nothing runs before all of it was checked, an output over another tensor's rows among that
+    pos, freqs = torch.zeros(3, dtype=torch.int32), torch.ones(64, dtype=torch.float64)
+    q, k, v = torch.zeros(1, 4, 3, 128), torch.zeros(1, 2, 3, 128), torch.zeros(1, 2, 3, 128, dtype=torch.bfloat16)
+    Q, K, V = bsa.rotary(q, k, v, pos, freqs, q_weight=torch.ones(128))
+    assert Q.shape == q.shape and K.shape == k.shape and V.dtype == v.dtype
+    assert len(launches) == 1 and launches[0][0] in ("bsa_rotary", "bsa_rotary_each")
+    assert [a is not None for a in launches[0][2]] == [True] * 6 + [False] + [True] * 4
+    bsa.rotary(q, k, None, pos, freqs)
+    bsa.rotary(q, q.clone(), q.clone(), pos, freqs)
+    assert len(launches) == 3
