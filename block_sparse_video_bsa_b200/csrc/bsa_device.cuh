@@ -185,6 +185,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// mbar_wait by a whole warp: one answer for all of its lanes.  Lanes come out of
+// a wait on their own, and where it runs out some may have seen the flag and
+// some the completion; what follows has barriers that count the warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
 // ------------------------------------------------------------------ TMA
 
 // 3-D tiled load global -> shared, completion counted on `bar` in bytes.

@@ -57,7 +57,7 @@ struct FewSmem {
   static constexpr uint32_t kBytes = kCtl + 512 + 1024;   // control, base alignment
 };
 struct FewCtl {
-  uint64_t full[8], empty[8], acc_full;
+  uint64_t full[8], empty[8], acc_full, fin;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -70,6 +70,12 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr)
                : "memory");
+  return v;
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
       mbar_init(&ctl->empty[i], 1);
     }
     mbar_init(&ctl->acc_full, 1);
+    mbar_init(&ctl->fin, 1);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -145,11 +152,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
       mma_commit(&ctl->empty[stage]);
       if (++stage == kRing) stage = 0, ++round;
     }
-    if (ok) mma_commit(&ctl->acc_full);
+    if (ok) {
+      mma_commit(&ctl->acc_full);
+    } else {   // those that were issued end before TMEM is freed
+      mma_commit(&ctl->fin);
+      mbar_wait(&ctl->fin, 0, wc);
+    }
   } else if (warp < 4) {
     // this share's sums, [token][channel]
-    if (mbar_wait(&ctl->acc_full, 0, wc)) {
-      __syncwarp();
+    if (mbar_wait_warp(&ctl->acc_full, 0, wc)) {
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
@@ -166,7 +177,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
   tc_fence_before();
   __syncthreads();
   if (split > 1) cluster_sync();
-  if (warp < 4) {
+  // sums of a CTA whose waits ran out are none: its cluster leaves the tile unwritten
+  const int ran_out = lane < split ? ld_cluster_s32(map_to_rank(&ctl->abort_flag, lane)) : 0;
+  if (warp < 4 && __all_sync(0xffffffffu, ran_out == 0)) {
     // warp w of rank q finishes tokens q + split (w + 4 i), four neighbouring channels a lane
     const int ch = r * kRowTile + 4 * lane;
     float ws[4], cb[4];
@@ -262,7 +275,7 @@ struct PairSmem {
   static constexpr uint32_t kBytes = kCtl + 512 + 1024;
 };
 struct PairCtl {
-  uint64_t full[12], empty[12], acc_full[2], acc_empty[2];
+  uint64_t full[12], empty[12], acc_full[2], acc_empty[2], fin;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -368,6 +381,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&ctl->acc_full[i], 1);
       mbar_init(&ctl->acc_empty[i], 16); // rank 0's: the epilogue warps of both
     }
+    mbar_init(&ctl->fin, 1);
     ctl->abort_flag = 0;
     fence_barrier_init();
   }
@@ -417,7 +431,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     bool ok = true;
     for (int64_t t = pair; t < tiles && ok; t += pairs, ++it) {
       const int buf = it & 1;
-      if (it >= 2 && !mbar_wait(&ctl->acc_empty[buf], ((it >> 1) - 1) & 1, wc)) break;
+      if (it >= 2 && !mbar_wait(&ctl->acc_empty[buf], ((it >> 1) - 1) & 1, wc)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       for (int k = 0; k < slices; ++k) {
         if (!mbar_wait(&ctl->full[stage], round & 1, wc)) {
@@ -434,6 +451,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         if (++stage == kRing) stage = 0, ++round;
       }
       if (ok) mma_commit_pair(&ctl->acc_full[buf]);
+    }
+    if (!ok) {   // those that were issued end before TMEM is freed
+      mma_commit_pair(&ctl->fin);
+      mbar_wait(&ctl->fin, 0, wc);
     }
   } else if (warp < 8) {
     // warps w and w + 4 share TMEM lanes 32 (w % 4) .. + 31, some of the columns each
@@ -462,8 +483,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
       }
-      if (!mbar_wait(&ctl->acc_full[buf], (it >> 1) & 1, wc)) break;
-      __syncwarp();
+      if (!mbar_wait_warp(&ctl->acc_full[buf], (it >> 1) & 1, wc)) break;
       tc_fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kBuf;
 #pragma unroll 1

@@ -3,6 +3,8 @@ frequency helper, and the refusals that come before any launch."""
 
 import ctypes
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -519,3 +521,19 @@ def test_rotary_of_several_layouts_is_one_call(launches):
     bsa.rotary(q, k, None, pos, freqs)
     bsa.rotary(q, q.clone(), q.clone(), pos, freqs)
     assert len(launches) == 3
+
+
+def test_warps_of_the_product_wait_as_one():
+    # a wait that runs out is answered lane by lane; barriers that count a warp follow, so all its lanes have to go on or none
+    text = open(os.path.join(os.path.dirname(bsa.__file__), "csrc", "linear_int8.cu")).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    for kernel in re.split(r"__global__", text)[1:]:
+        # the warps that read accumulators: after the producer's and the issuer's branches
+        warps = kernel[kernel.index("} else if (warp < "):]
+        assert re.findall(r"mbar_wait\w*\(&ctl->(\w+)", warps) == ["acc_full"] and "mbar_wait_warp(&ctl->acc_full" in warps
+    # sums are used only where no CTA of the cluster gave up
+    few = text[text.index("linear_int8_few_kernel("):text.index("int few_split")]
+    assert few.index("map_to_rank(&ctl->abort_flag") < few.index("a.w_scale")
+    # and multiplications that were issued are waited for before their accumulators are freed
+    for kernel in re.split(r"__global__", text)[1:]:
+        assert kernel.index("&ctl->fin, 0, wc") < kernel.index("tmem_dealloc")
