@@ -710,9 +710,10 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
     outs = out if out is not None else (None, None, None)
     # plain numbers: a key that held the caller's object (a tensor of no dimension) would
     # match by identity and keep its first value
-    eps, scale, inverse = float(eps), float(scale), bool(inverse)
+    if type(eps) is not float or type(scale) is not float or type(inverse) is not bool:
+        eps, scale, inverse = float(eps), float(scale), bool(inverse)
     if axis_pairs is not None:
-        axis_pairs = tuple([operator.index(n) for n in axis_pairs])
+        axis_pairs = tuple(map(operator.index, axis_pairs))
     host = _host or _load_host()
     key = (host.layout(q, k, v, *outs, positions, freqs, q_weight, k_weight), layout, axis_pairs,
            eps, scale, inverse, out_dtype)
@@ -790,8 +791,11 @@ def gate_norm(x, y=None, gate=None, scale=None, shift=None, pre="rms", pre_weigh
     [C].  quantize: z is (codes [B N, C] int8, scales [B N]) for ``linear_int8``.  h_out: where h
     goes (x for an update in place).  want_z=False: z is None and only h is made."""
     host = _host or _load_host()
-    eps, residual_scale, branch_scale = float(eps), float(residual_scale), float(branch_scale)
-    quantize, want_z = bool(quantize), bool(want_z)      # plain values in the key, as in rotary
+    if (type(eps) is not float or type(residual_scale) is not float
+            or type(branch_scale) is not float or type(quantize) is not bool
+            or type(want_z) is not bool):                # plain values in the key, as in rotary
+        eps, residual_scale, branch_scale = float(eps), float(residual_scale), float(branch_scale)
+        quantize, want_z = bool(quantize), bool(want_z)
     key = (host.layout(x, y, gate, scale, shift, post_weight, post_bias, pre_weight, pre_bias,
                        h_out), pre, post, eps, residual_scale, branch_scale, quantize, z_dtype,
            want_z)

@@ -2,6 +2,7 @@
 // argument checks, tensor maps and launches.  No memory is allocated and no
 // state kept.
 #include <cmath>
+#include <functional>
 
 #include "api_util.h"
 #include "bsa.h"
@@ -63,10 +64,12 @@ struct Rows {
   const void* base;
   int size;
   int64_t row, n[3], s[3];
+  Range range;
+  Rows(const void* base, int size, int64_t row, int64_t n0, int64_t s0, int64_t n1, int64_t s1,
+       int64_t n2 = 1, int64_t s2 = 0)
+      : base(base), size(size), row(row), n{n0, n1, n2}, s{s0, s1, s2},
+        range(range_of(base, size, row, n0, s0, n1, s1, n2, s2)) {}
 };
-Range range_of(const Rows& r) {
-  return range_of(r.base, r.size, r.row, r.n[0], r.s[0], r.n[1], r.s[1], r.n[2], r.s[2]);
-}
 
 // Some row of `bytes`, `at` bytes past one of the same shape, meets one of these
 // rows: strides in bytes, the largest last, each at least what the smaller ones
@@ -84,8 +87,7 @@ bool rows_meet(int64_t at, int64_t bytes, const int64_t* n, const int64_t* s, in
 // No byte belongs to both: their ranges lie apart, or they are rows of one shape
 // that interleave (views of one buffer).
 bool apart(const Rows& a, const Rows& b) {
-  const Range ra = range_of(a), rb = range_of(b);
-  if (!meet(ra, rb)) return true;
+  if (!meet(a.range, b.range)) return true;
   bool same = a.size == b.size && a.row == b.row;
   for (int i = 0; i < 3; ++i)
     same = same && a.n[i] == b.n[i] && (a.n[i] == 1 || a.s[i] == b.s[i]);
@@ -99,7 +101,7 @@ bool apart(const Rows& a, const Rows& b) {
         order[i] = order[j], order[j] = t;
       }
   for (int i = 0; i < 3; ++i) n[i] = a.n[order[i]], s[i] = a.s[order[i]] * a.size;
-  return !rows_meet(static_cast<int64_t>(rb.lo - ra.lo), a.row * a.size, n, s, 3);
+  return !rows_meet(static_cast<int64_t>(b.range.lo - a.range.lo), a.row * a.size, n, s, 3);
 }
 
 // Each entry checks its arguments and, with `launch`, enqueues its kernel: a
@@ -158,16 +160,17 @@ int rotary_entry(const bsa_rotary_params* params, const void* q, const void* k, 
   if (p->rotary_dim > 0 && (q || k) && (!positions || !freqs)) return BSA_ERR_INVALID;
   // Outputs: on their own input exactly, or apart from every input and output.
   auto ins = [&](int i) {
-    return Rows{a.in[i], si, 128, {p->B, p->H, p->N}, {p->in_b, p->in_h, p->in_n}};
+    return Rows(a.in[i], si, 128, p->B, p->in_b, p->H, p->in_h, p->N, p->in_n);
   };
   auto outs = [&](int i) {
-    return Rows{a.out[i], so, 128, {p->B, p->H, p->N}, {p->out_b, p->out_h, p->out_n}};
+    return Rows(a.out[i], so, 128, p->B, p->out_b, p->H, p->out_h, p->N, p->out_n);
   };
+  const Rows rin[3] = {ins(0), ins(1), ins(2)}, rout[3] = {outs(0), outs(1), outs(2)};
   for (int i = 0; i < a.ntens; ++i)
     for (int j = 0; j < a.ntens; ++j) {
       const bool in_place = i == j && a.out[i] == a.in[i] && same;
-      if (!in_place && !apart(outs(i), ins(j))) return BSA_ERR_INVALID;
-      if (j > i && !apart(outs(i), outs(j))) return BSA_ERR_INVALID;
+      if (!in_place && !apart(rout[i], rin[j])) return BSA_ERR_INVALID;
+      if (j > i && !apart(rout[i], rout[j])) return BSA_ERR_INVALID;
     }
   for (int i = 0; i < a.ntens; ++i)
     if (!aligned(a.in[i], 16) || !aligned(a.out[i], 16) ||
@@ -206,8 +209,8 @@ int rotary_each_entry(const bsa_rotary_params* p, const void* const (&in)[3],
   auto rows = [&](int i, bool input) {
     const bsa_rotary_params& r = p[i];
     const int size = type_size(input ? r.in_dtype : r.out_dtype);
-    if (input) return Rows{in[i], size, 128, {r.B, r.H, r.N}, {r.in_b, r.in_h, r.in_n}};
-    return Rows{out[i], size, 128, {r.B, r.H, r.N}, {r.out_b, r.out_h, r.out_n}};
+    if (input) return Rows(in[i], size, 128, r.B, r.in_b, r.H, r.in_h, r.N, r.in_n);
+    return Rows(out[i], size, 128, r.B, r.out_b, r.H, r.out_h, r.N, r.out_n);
   };
   auto alike = [](const Rows& a, const Rows& b) {
     bool same = a.size == b.size;
@@ -295,7 +298,7 @@ int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inpu
   // output is refused, with the vectors too: one a token is as large as the rows,
   // and is read after other rows were written.
   auto rows = [&](const void* base, int size, int64_t sb, int64_t sn) {
-    return Rows{base, size, p->C, {p->B, p->N, 1}, {sb, sn, 0}};
+    return Rows(base, size, p->C, p->B, sb, p->N, sn);
   };
   const Rows x = rows(in->x, sx, p->x_b, p->x_n), y = rows(in->y, sy, p->y_b, p->y_n);
   const Rows ho = rows(h, sx, p->h_b, p->h_n), zo = rows(z, sz, p->z_b, p->z_n);
@@ -306,7 +309,7 @@ int gate_norm_entry(const bsa_gate_norm_params* params, const bsa_gate_norm_inpu
                            rows(in->pre_weight, 4, 0, 0), rows(in->pre_bias, 4, 0, 0)};
   const bool in_place = h == in->x && p->h_b == p->x_b && p->h_n == p->x_n;
   if (h && z && !apart(ho, zo)) return BSA_ERR_INVALID;
-  for (const Rows& o : {ho, zo}) {
+  for (const Rows& o : {std::cref(ho), std::cref(zo)}) {
     if (!o.base) continue;
     if (!(o.base == h && in_place) && !apart(o, x)) return BSA_ERR_INVALID;
     if (in->y && !apart(o, y)) return BSA_ERR_INVALID;
