@@ -252,7 +252,8 @@ __device__ __forceinline__ float2 combine_moments(RowGroup& g, float mean, float
   if (g.warps() == 1) return make_float2(mean, q * inv);
   const float4 p = row_partials(g, make_float4(mean, q, cnt, 0.f));
   const float all = warp_sum(p.x * p.z) * inv;
-  const float d = p.x - all;
+  // nothing from lanes that stand for no values: their distance may square past fp32
+  const float d = p.z > 0.f ? p.x - all : 0.f;
   return make_float2(all, warp_sum(fmaf(d * d, p.z, p.y)) * inv);
 }
 

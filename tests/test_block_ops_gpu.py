@@ -706,3 +706,14 @@ def test_linear_int8_tiles_of_every_width(cuda_dev, M, K, N, out):
     # the sum (exact below 2^24), its product with a_scale, the fused step and the last rounding: half a step each
     room = 2.0**-23 * scaled.abs() + 2.0**-24 * want.abs() + torch.finfo(out).eps / 2 * (want.abs() + 2.0**-22 * scaled.abs()) + 1e-30
     assert ((got - want).abs() <= room).all()
+
+
+@pytest.mark.parametrize("N,C", [(3, 512), (2, 7_168), (3, 1_111), (2, 24_000), (3_000, 7_168), (40_000, 264)])
+def test_layer_norm_of_rows_far_from_zero(cuda_dev, N, C):
+    # the square of the mean is past fp32, the deviations are not
+    x = 1e20 + 1e17 * rnd(820, 1, N, C)
+    _, z = bsa.gate_norm(x, pre="layer", z_dtype=torch.float32)
+    assert z.isfinite().all()
+    rows = [0, 1, N - 1]
+    _, zr, _, ez = gate_norm_bounds(x[:, rows], None, None, None, None, "layer", "none", [None] * 4, 1e-6, 1.0, 1.0)
+    close(z[:, rows], zr, ez)
