@@ -336,7 +336,11 @@ __device__ __forceinline__ float2 row_affine(RowGroup& g, int n, int kind, float
   }
   const float2 mv = combine_moments(g, mean, warp_sum(q), cnt, n);
   const float r = rsqrtf(mv.y + eps);
-  return make_float2(-mv.x * r, r);
+  const float m = -mv.x * r;
+  // m past fp32 with a finite r: a deviation is 2^-24 of the mean at least, which
+  // would hold |m| below 2^24 sqrt(n), so there is none and the norm is 0
+  if (fabsf(m) == INFINITY && r < INFINITY) return make_float2(0.f, 0.f);
+  return make_float2(m, r);
 }
 
 template <class Tx, class Ty, int CH>

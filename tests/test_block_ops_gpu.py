@@ -717,3 +717,17 @@ def test_layer_norm_of_rows_far_from_zero(cuda_dev, N, C):
     rows = [0, 1, N - 1]
     _, zr, _, ez = gate_norm_bounds(x[:, rows], None, None, None, None, "layer", "none", [None] * 4, 1e-6, 1.0, 1.0)
     close(z[:, rows], zr, ez)
+
+
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("N,C", [(3, 512), (1, 8_192), (3_000, 8_192), (40_000, 256), (2_000, 2_048)])
+def test_layer_norm_of_one_large_value(cuda_dev, N, C, post):
+    # sums of a power of two are exact, so there is no deviation and z is 0, although the value over the smallest
+    # root (10^7 times it) is past fp32
+    x = torch.full((1, N, C), 2.0 ** 110, device="cuda")
+    if post:
+        h, z = bsa.gate_norm(torch.zeros_like(x), x, pre="none", post="layer", eps=1e-14, z_dtype=torch.float32)
+        assert not h.any()
+    else:
+        _, z = bsa.gate_norm(x, pre="layer", eps=1e-14, z_dtype=torch.float32)
+    assert not z.any()
