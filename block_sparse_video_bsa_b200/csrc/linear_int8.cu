@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
     float ws[4], cb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      ws[j] = ch + j < a.N ? __ldg(a.w_scale + ch + j) : 0.f;
-      cb[j] = ch + j < a.N && a.bias ? __ldg(a.bias + ch + j) : 0.f;
+      ws[j] = ch + j < a.N ? a.w_scale[ch + j] : 0.f;
+      cb[j] = ch + j < a.N && a.bias ? a.bias[ch + j] : 0.f;
     }
     for (int m = rank + split * warp; m < kCols && m < a.M; m += 4 * split) {
       int4 sum = make_int4(0, 0, 0, 0);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) linear_int8_few_kernel(
           }
         }
       }
-      const float rs = __ldg(a.a_scale + m);
+      const float rs = a.a_scale[m];
       const float o[4] = {fmaf(static_cast<float>(sum.x) * rs, ws[0], cb[0]),
                           fmaf(static_cast<float>(sum.y) * rs, ws[1], cb[1]),
                           fmaf(static_cast<float>(sum.z) * rs, ws[2], cb[2]),
@@ -339,8 +339,8 @@ __device__ __forceinline__ void finish_block(const LinearInt8Args& a, int64_t ro
   for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = static_cast<float>(static_cast<int32_t>(v[j])) * rs;
   __syncwarp();
   const bool in = col + lane < a.N;
-  const float cs = in ? __ldg(a.w_scale + col + lane) : 0.f;
-  const float cb = in && a.bias ? __ldg(a.bias + col + lane) : 0.f;
+  const float cs = in ? a.w_scale[col + lane] : 0.f;
+  const float cb = in && a.bias ? a.bias[col + lane] : 0.f;
   const int64_t at = row0 * a.ldo + col + lane;
   const int rows = in ? static_cast<int>(a.M - row0 < 32 ? a.M - row0 : 32) : 0;
   auto put = [&](auto* p) {
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
       tile_of(t, row_tiles, col_tiles, &r, &c);
       const int64_t row = static_cast<int64_t>(r) * kPairRows + rank * 128 + quad * 32 + lane;
       const bool row_ok = row < a.M;
-      const float rs = row_ok ? __ldg(a.a_scale + row) : 0.f;
+      const float rs = row_ok ? a.a_scale[row] : 0.f;
       if (wide) {
         // this warp's columns' scales and biases, on their way while the tile accumulates
         float* tab = stage;
@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         if (4 * lane < kSide) {
           float4 cs = make_float4(0.f, 0.f, 0.f, 0.f), cb = cs;
           if (col + 4 <= a.N) {
-            cs = __ldg(reinterpret_cast<const float4*>(a.w_scale + col));
-            if (a.bias) cb = __ldg(reinterpret_cast<const float4*>(a.bias + col));
+            cs = *reinterpret_cast<const float4*>(a.w_scale + col);
+            if (a.bias) cb = *reinterpret_cast<const float4*>(a.bias + col);
           }
           reinterpret_cast<float4*>(tab)[lane] = cs;
           reinterpret_cast<float4*>(tab + kTable)[lane] = cb;

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) quant_int8_bf16_kernel(cons
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       w[c] = make_uint4(0, 0, 0, 0);
-      if (row_index<kAligned>(g, c, 0) < n) w[c] = ld_stream_v4(src + off[c]);
+      if (row_index<kAligned>(g, c, 0) < n) w[c] = ld_row_v4(src + off[c]);
     }
     uint32_t m = 0;
 #pragma unroll

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a)
   uint64_t* steps64 = reinterpret_cast<uint64_t*>(&ring[kDepth - 1][0][0]);
   if (turns) {
     if (static_cast<int>(threadIdx.x) < half) {
-      const double f = __ldg(a.freqs + threadIdx.x) * 0.15915494309189533577;   // turns a position
+      const double f = a.freqs[threadIdx.x] * 0.15915494309189533577;   // turns a position
       steps64[threadIdx.x] =
           static_cast<uint64_t>(__double2ll_rn((f - rint(f)) * 18446744073709551616.0));
     }
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a)
       int axis = 0;
       while (i >= a.axis_end[axis]) ++axis;
       const uint64_t phase =
-          steps64[i] * static_cast<uint64_t>(static_cast<int64_t>(__ldg(pos + axis)));
+          steps64[i] * static_cast<uint64_t>(static_cast<int64_t>(pos[axis]));
       // [-2^31, 2^31) of a turn in 2^-32 units -> half turns in [-1, 1)
       sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, sn, cs);
       *cs *= a.scale;
@@ -205,8 +205,8 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a)
     };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      c0[j] *= __ldg(w + e0 + j), s0[j] *= __ldg(w + partner(e0 + j));
-      c1[j] *= __ldg(w + e1 + j), s1[j] *= __ldg(w + partner(e1 + j));
+      c0[j] *= w[e0 + j], s0[j] *= w[partner(e0 + j)];
+      c1[j] *= w[e1 + j], s1[j] *= w[partner(e1 + j)];
     }
   }
   const bool part = r < kDim;   // some dimensions pass

@@ -118,12 +118,12 @@ __device__ __forceinline__ void load_row(const RowGroup& g, const T* p, int n, f
 }
 
 __device__ __forceinline__ void shared_words(const float* p, float v[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 __device__ __forceinline__ void shared_words(const __nv_bfloat16* p, float v[8]) {
-  bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p)), v);
+  bf16x8_to_f32(*reinterpret_cast<const uint4*>(p), v);
 }
 // 8 neighbours at p, which starts anywhere: from the aligned words around them
 // (which lie inside the vector: `room` says so) by a shift that all threads of
@@ -132,9 +132,9 @@ __device__ __forceinline__ void shared_words(const __nv_bfloat16* p, float v[8])
 __device__ __forceinline__ void around8(const float* p, float v[8]) {
   const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 2) & 3u;
   const float4* q = reinterpret_cast<const float4*>(p - off);
-  const float4 a = __ldg(q), b = __ldg(q + 1);
+  const float4 a = *q, b = q[1];
   float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (off) c = __ldg(q + 2);
+  if (off) c = q[2];
   float w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
 #pragma unroll
   for (int j = 0; j < 10; ++j) w[j] = off & 2u ? w[j + 2] : w[j];
@@ -148,9 +148,9 @@ __device__ __forceinline__ bool room(const float* p, int i, int n) {
 __device__ __forceinline__ void around8(const __nv_bfloat16* p, float v[8]) {
   const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) >> 1) & 7u;
   const uint4* q = reinterpret_cast<const uint4*>(p - off);
-  const uint4 a = __ldg(q);
+  const uint4 a = *q;
   uint4 b = make_uint4(0, 0, 0, 0);
-  if (off) b = __ldg(q + 1);
+  if (off) b = q[1];
   uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int j = 0; j < 6; ++j) w[j] = off & 4u ? w[j + 2] : w[j];

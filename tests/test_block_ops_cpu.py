@@ -537,3 +537,15 @@ def test_warps_of_the_product_wait_as_one():
     # and multiplications that were issued are waited for before their accumulators are freed
     for kernel in re.split(r"__global__", text)[1:]:
         assert kernel.index("&ctl->fin, 0, wc") < kernel.index("tmem_dealloc")
+
+
+@pytest.mark.parametrize("name", ["rotary.cu", "gate_norm.cu", "quant_int8.cu", "linear_int8.cu", "rows.cuh"])
+def test_kernels_that_start_early_read_through_the_coherent_path(name):
+    # A kernel that is resident while the one before it still writes may not use read-only loads: they hold for memory that
+    # nobody writes during the kernel's life, and nothing orders them after the wait.
+    text = open(os.path.join(os.path.dirname(bsa.__file__), "csrc", name)).read()
+    text = re.sub(r"//[^\n]*", "", text)
+    for word in ("__ldg", "ld.global.nc", "ld_stream_v4", "__ldcs", "__restrict__"):
+        assert word not in text, word
+    if name.endswith(".cu"):
+        assert text.count("__global__") == text.count("grid_wait();") == text.count("grid_ready();")

@@ -731,3 +731,45 @@ def test_layer_norm_of_one_large_value(cuda_dev, N, C, post):
     else:
         _, z = bsa.gate_norm(x, pre="layer", eps=1e-14, z_dtype=torch.float32)
     assert not z.any()
+
+
+@pytest.mark.parametrize("B,N,C", [(1, 1, 7_168), (3, 40, 1_111), (2, 700, 2_048), (1, 5_000, 640)])
+def test_vectors_made_by_the_call_before(cuda_dev, B, N, C):
+    # gate, scale and shift come from a projection and the weights, scales and biases from norms, over and over into the same
+    # places, and are read by the very next call
+    x, y = rnd(830, B, N, C), rnd(831, B, N, C)
+    emb = rnd(832, 1, B, 256)
+    w, sw = bsa.quantize_int8(rnd(833, 3 * C, 256))
+    mod, w128 = torch.empty(B, 3 * C, device="cuda"), torch.empty(1, 1, 128, device="cuda")
+    wa, sa = bsa.quantize_int8(rnd(834, 128, C, scale=C ** -0.5))
+    ones = torch.ones(128, device="cuda")
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    freqs, _ = bsa.rotary_freqs(64)
+
+    def chain(wait):
+        e, outs = emb.clone(), []
+        for i in range(6):
+            _, (a, s) = bsa.gate_norm(e, quantize=True)
+            wait()
+            bsa.linear_int8(a, s, w, sw, out=mod)
+            wait()
+            gate, scale, shift = (mod[:, j * C:(j + 1) * C] for j in range(3))
+            _, (a, s) = bsa.gate_norm(x, y, gate, scale, shift, post="rms", quantize=True)
+            wait()
+            q = bsa.linear_int8(a, s, wa, sa, ones, torch.float32)
+            wait()
+            q = q.view(B, N, 1, 128).transpose(1, 2)
+            h, _ = bsa.gate_norm(q[:1, 0, :1], q[:1, 0, -1:], h_out=w128, pre="none", post="rms", want_z=False)
+            wait()
+            Q, _, _ = bsa.rotary(q, None, None, pos, freqs, q_weight=w128.view(128))
+            wait()
+            h, z = bsa.gate_norm(Q[:1, 0], pre="rms", pre_weight=w128.view(128), pre_bias=w128.view(128), z_dtype=torch.float32)
+            wait()
+            outs += [mod.clone(), w128.clone(), Q, z]
+            e = e * 0.5 + Q[:, 0, 0, :1].reshape(1, B, 1)
+        return outs
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(10):
+        for a, b in zip(chain(lambda: None), want):
+            assert torch.equal(a, b)
