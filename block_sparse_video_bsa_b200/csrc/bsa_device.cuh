@@ -194,8 +194,7 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
 
 // ------------------------------------------------------------------ TMA
 
-// 3-D tiled load global -> shared, completion counted on `bar` in bytes.
-// c0 (innermost, elements) must keep c0 * sizeof(elem) a multiple of 16.
+// 2-D tiled load global -> shared, as tma_load_3d.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1) {
   asm volatile(
@@ -205,6 +204,8 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 3-D tiled load global -> shared, completion counted on `bar` in bytes.
+// c0 (innermost, elements) must keep c0 * sizeof(elem) a multiple of 16.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int c0, int c1, int c2) {
   asm volatile(

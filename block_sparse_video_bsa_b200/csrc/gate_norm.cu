@@ -729,8 +729,7 @@ cudaError_t launch(const GateNormArgs& a, int ch, int threads, int blocks, cudaS
   if (ch == 1) return go(gate_norm_kernel<Tx, 1, 1024, 1, kMode>);
   if (ch == 2) return threads <= 512 ? go(gate_norm_kernel<Tx, 2, 512, 2, kMode>)
                                      : go(gate_norm_kernel<Tx, 2, 1024, 1, kMode>);
-  return threads <= 512 ? go(gate_norm_kernel<Tx, 4, 512, 1, kMode>)
-                        : go(gate_norm_kernel<Tx, 4, 1024, 1, kMode>);
+  return go(gate_norm_kernel<Tx, 4, 1024, 1, kMode>);   // rows past 16,384 values: over 512 threads
 }
 
 }  // namespace

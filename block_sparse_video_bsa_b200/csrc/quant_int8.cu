@@ -129,9 +129,7 @@ cudaError_t launch_quant_int8(const QuantInt8Args& a, bool x_fp32, bool vec, cud
     if (threads <= 256) return go(quant_int8_bf16_kernel<4, 256, 6>);
     return go(quant_int8_bf16_kernel<4, 1024, 1>);
   }
-  if (vec)
-    return x_fp32 ? launch<float, kAligned>(a, ch, threads, blocks, st)
-                  : launch<__nv_bfloat16, kAligned>(a, ch, threads, blocks, st);
+  if (vec) return launch<float, kAligned>(a, ch, threads, blocks, st);
   return x_fp32 ? launch<float, kSingles>(a, ch, threads, blocks, st)
                 : launch<__nv_bfloat16, kSingles>(a, ch, threads, blocks, st);
 }
