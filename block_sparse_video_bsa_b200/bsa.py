@@ -558,13 +558,21 @@ _host = None
 
 
 def _load_host():
-    """The extension module built from csrc/host.cpp (raises if it was not built)."""
+    """The extension module built from csrc/host.cpp (raises if it was not built, or for another
+    torch or Python)."""
     global _host
     if _host is None:
+        from .build import host_built_for
+        again = "run `python -m block_sparse_video_bsa_b200.build`"
         if not os.path.exists(os.path.join(os.path.dirname(os.path.abspath(__file__)), "_host.so")):
-            raise RuntimeError("_host.so is missing: run `python -m "
-                               "block_sparse_video_bsa_b200.build` first")
-        from . import _host as module
+            raise RuntimeError(f"_host.so is missing: {again} first")
+        try:
+            from . import _host as module
+        except ImportError as e:      # a symbol of another torch
+            raise RuntimeError(f"_host.so does not load ({e}): {again} again") from e
+        if getattr(module, "built_for", None) != host_built_for():
+            raise RuntimeError(f"_host.so was built for {getattr(module, 'built_for', 'another torch')}, this is "
+                               f"{host_built_for()}: {again} again")
         _host = module
     return _host
 
@@ -606,8 +614,10 @@ def _elsewhere(device, stream, where):
     return torch.cuda.stream(stream)
 
 
-_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# torch's own accessors; the public ones where a torch lacks these (a few tenths of a us more)
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
 def _here(device, stream):

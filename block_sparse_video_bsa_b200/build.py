@@ -19,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsa.so")
 HOST = os.path.join(PKG, "_host.so")
 BUILD_DIR = os.path.join(PKG, "_build")
+HOST_STAMP = os.path.join(BUILD_DIR, "host.built_for")
 SOURCES = ["api.cu", "pool_summarize.cu", "select.cu", "attend.cu", "attend_fp8.cu", "quant_fp8.cu",
            "reblock.cu", "extra.cu", "noalloc.cu", "api_block.cu", "rotary.cu", "gate_norm.cu",
            "quant_int8.cu", "linear_int8.cu"]
@@ -46,6 +47,12 @@ def _newer(target: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def host_built_for() -> str:
+    """What _host.so depends on beside its source: it is compiled against torch's and Python's C++ headers."""
+    import torch
+    return f"torch {torch.__version__}, Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
 def _host_command(source: str) -> list:
     import sysconfig
 
@@ -53,10 +60,20 @@ def _host_command(source: str) -> list:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DBSA_BUILT_FOR="{host_built_for()}"',
             "-I", os.path.join(os.path.dirname(lib), "include"),
             "-I", os.path.join(os.path.dirname(lib), "include", "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], source,
             "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", "-o", HOST]
+
+
+def _host_current(source: str) -> bool:
+    """_host.so was made from this source, for this torch and Python."""
+    try:
+        with open(HOST_STAMP) as f:
+            return _newer(HOST, [source]) and f.read() == host_built_for()
+    except OSError:
+        return False
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
@@ -74,7 +91,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
             jobs.append([nvcc, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o])
 
     source = os.path.join(CSRC, "host.cpp")
-    if force or not _newer(HOST, [source]):
+    host = force or not _host_current(source)
+    if host:
         jobs.append(_host_command(source))
 
     def run(cmd):
@@ -88,6 +106,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
 
     with cf.ThreadPoolExecutor(max_workers=len(jobs) or 1) as ex:
         list(ex.map(run, jobs))
+    if host:
+        with open(HOST_STAMP, "w") as f:
+            f.write(host_built_for())
     if force or not _newer(LIB, objs):
         run([nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", LIB])
     return LIB

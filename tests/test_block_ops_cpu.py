@@ -549,3 +549,36 @@ def test_kernels_that_start_early_read_through_the_coherent_path(name):
         assert word not in text, word
     if name.endswith(".cu"):
         assert text.count("__global__") == text.count("grid_wait();") == text.count("grid_ready();")
+
+
+def test_host_module_is_tied_to_its_torch_and_python(monkeypatch, tmp_path):
+    from block_sparse_video_bsa_b200 import build
+    module = bsa._load_host()
+    assert module.built_for == build.host_built_for() and torch.__version__ in module.built_for
+    source, made, stamp = (str(tmp_path / n) for n in ("host.cpp", "host.so", "stamp"))
+    monkeypatch.setattr(build, "HOST", made)
+    monkeypatch.setattr(build, "HOST_STAMP", stamp)
+    for path, text in ((source, ""), (made, ""), (stamp, module.built_for)):
+        assert not build._host_current(source)
+        with open(path, "w") as f:
+            f.write(text)
+    assert build._host_current(source)
+    monkeypatch.setattr(build, "host_built_for", lambda: "torch 0.0, Python 0.0")
+    assert not build._host_current(source)                                   # built again
+    monkeypatch.setattr(bsa, "_host", None)
+    with pytest.raises(RuntimeError, match="torch 0.0, Python 0.0"):         # and not used before that
+        bsa._load_host()
+
+
+def test_wrappers_have_a_device_and_a_stream_on_every_torch():
+    # under a torch without the private accessors
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    hasattr(torch._C, n) and delattr(torch._C, n)\n"
+            "from block_sparse_video_bsa_b200 import bsa\n"
+            "assert callable(bsa._device_now) and callable(bsa._raw_stream)\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(bsa.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
