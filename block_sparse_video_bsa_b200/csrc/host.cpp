@@ -84,7 +84,7 @@ bool address(PyObject* o, void** out) {
   if (o == Py_None) {
     *out = nullptr;
   } else if (THPVariable_Check(o)) {
-    *out = const_cast<void*>(THPVariable_Unpack(o).const_data_ptr());
+    *out = THPVariable_Unpack(o).mutable_data_ptr();   // of its own, where a lazy clone shares memory
   } else {
     *out = PyLong_AsVoidPtr(o);
     return !PyErr_Occurred();

@@ -582,3 +582,15 @@ def test_wrappers_have_a_device_and_a_stream_on_every_torch():
     root = os.path.dirname(os.path.dirname(os.path.abspath(bsa.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_host_calls_get_a_tensor_of_its_own():
+    # a lazy clone shares its source's memory until it is written: an output's address has to be its own
+    if not hasattr(torch.Tensor, "_lazy_clone"):
+        pytest.skip("this torch has no lazy clones")
+    seen = []
+    record = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 5)(lambda *a: seen.extend(a) or 0)
+    x = torch.zeros(64)
+    y = x._lazy_clone()
+    assert bsa._load_host().call(ctypes.cast(record, ctypes.c_void_p).value, y, None, None, None, None) == 0
+    assert seen[0] == y.data_ptr() != x.data_ptr() and seen[1:] == [None] * 4
