@@ -773,3 +773,71 @@ def test_vectors_made_by_the_call_before(cuda_dev, B, N, C):
     for _ in range(10):
         for a, b in zip(chain(lambda: None), want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("form", ["scale", "shift", "both", "both a token", "weight and bias", "gate", "gate a token"])
+@pytest.mark.parametrize("C,N,dtype", [(7_168, 4_000, torch.bfloat16), (2_048, 4_000, torch.float32), (256, 30_000, torch.bfloat16)])
+def test_gate_norm_rounds_the_same_for_few_and_many_rows(cuda_dev, C, N, dtype, form):
+    # without a norm there is no sum to order: the streamed kernel and the other one round every product and every sum
+    x, y = rnd(840, 1, N, C, dtype=dtype), rnd(841, 1, N, C, dtype=torch.bfloat16)
+    token = "token" in form
+    m = [rnd(842 + i, 1, N if token else 1, C, scale=0.3) for i in range(3)]
+    w, b = 1 + rnd(845, C, scale=0.1), rnd(846, C, scale=0.1)
+    f = x.float()
+
+    def call(rows, **kw):
+        v = [t[:, :rows] for t in m]
+        if "gate" in form:
+            return bsa.gate_norm(x[:, :rows], y[:, :rows], v[0], pre="none", **kw)
+        if "weight" in form:
+            return bsa.gate_norm(x[:, :rows], pre="none", pre_weight=w, pre_bias=b, **kw)
+        return bsa.gate_norm(x[:, :rows], None, None, None if form == "shift" else v[0], None if form == "scale" else v[1], "none", **kw)
+    want = {"gate": lambda: f + y.float() * m[0], "weig": lambda: f * w + b, "scal": lambda: f * (1 + m[0]), "shif": lambda: f + m[1],
+            "both": lambda: f * (1 + m[0]) + m[1]}[form[:4]]()
+    _, few = call(4, z_dtype=torch.float32)
+    _, many = call(N, z_dtype=torch.float32)
+    assert torch.equal(many, want) and torch.equal(few, want[:, :4])
+    _, (codes, top) = call(N, quantize=True)
+    c, t = bsa.quantize_int8(want[0])
+    assert torch.equal(codes, c) and torch.equal(top, t)
+    _, (codes, top) = call(4, quantize=True)
+    assert torch.equal(codes, c[:4]) and torch.equal(top, t[:4])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,C", [(4, 7_168), (4_000, 7_168), (4_000, 2_048), (30_000, 256), (3_000, 1_111)])
+def test_gate_norm_codes_of_special_rows(cuda_dev, N, C, dtype):
+    # rows that hold a NaN or an infinity, at a row's first, last and cut chunks; nothing of them shows in their neighbours
+    x = rnd(850, 1, N, C, dtype=dtype)
+    keep = x.clone()
+    bad = {0: (0, float("nan")), 1: (C - 1, float("inf")), N // 2: (C // 2, -float("inf")), N - 1: (C - 1, float("nan"))}
+    for row, (at, v) in bad.items():
+        x[0, row, at] = v
+    zero = [r for r in (2, N // 2 + 1, N - 3) if r not in bad][:1]
+    x[0, zero] = 0
+    keep[0, zero] = 0
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[list(bad)] = False
+    for pre in ("none", "rms", "layer"):
+        _, (codes, top) = bsa.gate_norm(x, pre=pre, quantize=True)
+        assert top[~rest].isnan().all() and not codes[~rest].any()
+        _, (c, t) = bsa.gate_norm(keep, pre=pre, quantize=True)
+        assert torch.equal(codes[rest], c[rest]) and torch.equal(top[rest], t[rest]) and t.isfinite().all()
+        assert not c[zero].any() and (t[zero] == np.float32(2.0 ** -100 / 127)).all()
+
+
+@pytest.mark.parametrize("N,C", [(3, 7_168), (4_000, 7_168), (4_000, 1_111), (30_000, 256)])
+def test_gate_norm_codes_differ_from_64_bits_at_borders_only(cuda_dev, N, C):
+    """The factor is right to 2^-18 (above) and enters the row's largest value too; product, sum, scale and code product round
+    once each: 127 (2^-17 + 8 2^-24), below 127 2^-16 of a code.  So a code is that of 64 bits, or the other one of a border
+    that the 64-bit value is this near to."""
+    x = (rnd(860, 1, N, C) * (1 + 9 * (rnd(861, C) > 2))).bfloat16()
+    scale, shift = (rnd(862 + i, 1, 1, C, scale=0.3) for i in range(2))
+    _, (codes, _) = bsa.gate_norm(x, None, None, scale, shift, quantize=True)
+    z = x[0].double()
+    z = z / (z.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    z = z * (1 + scale[0].double()) + shift[0].double()
+    exact = z * (127.0 / z.abs().amax(1, keepdim=True))
+    off = (codes.double() - exact).abs()
+    assert bool((off <= 0.5 + 127 * 2.0 ** -16).all())
+    assert bool(((codes.double() == exact.round()) | ((exact - exact.floor() - 0.5).abs() <= 127 * 2.0 ** -16)).all())
