@@ -841,3 +841,59 @@ def test_gate_norm_codes_differ_from_64_bits_at_borders_only(cuda_dev, N, C):
     off = (codes.double() - exact).abs()
     assert bool((off <= 0.5 + 127 * 2.0 ** -16).all())
     assert bool(((codes.double() == exact.round()) | ((exact - exact.floor() - 0.5).abs() <= 127 * 2.0 ** -16)).all())
+
+
+def test_captured_over_two_streams_that_join(cuda_dev):
+    # a graph whose branches fork and join around the calls: launches that start early wait for both sides
+    c = block_case(1, 700, 3, 512, 870)
+    B, N, C = c["x"].shape
+    H = c["w_out"].shape[1] // 128
+    freqs, pos = c["freqs"], c["positions"]
+    x = c["x"].clone()
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        _, (a, sa) = bsa.gate_norm(x, scale=c["scale"], shift=c["shift"], pre="layer", quantize=True)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            kv = bsa.linear_int8(a, sa, c["w_qkv"][H * 128:], c["s_qkv"][H * 128:]).view(B, N, 2, H, 128)
+            _, K, V = bsa.rotary(None, kv[:, :, 0].transpose(1, 2), kv[:, :, 1].transpose(1, 2), pos, freqs, "interleaved", [22, 21, 21])
+        q = bsa.linear_int8(a, sa, c["w_qkv"][:H * 128], c["s_qkv"][:H * 128]).view(B, N, H, 128)
+        Q, _, _ = bsa.rotary(q.transpose(1, 2), None, None, pos, freqs, "interleaved", [22, 21, 21])
+        main.wait_stream(side)
+        _, z = bsa.gate_norm(Q.view(1, -1, 128), V.view(1, -1, 128), gate=K.view(1, -1, 128), pre="none")
+        codes, s = bsa.quantize_int8(z.view(B, H, N, 128))
+        for t in (a, sa, kv, K, V):
+            t.record_stream(side)
+        return Q, K, V, z, codes, s
+
+    want = [t.clone() for t in step(torch.cuda.current_stream())]
+    torch.cuda.synchronize()
+    graph, stream, side = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step(side)
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_calls_from_two_threads(cuda_dev):
+    import threading
+    cs = [block_case(1, n, 3, 512, 880 + n) for n in (300, 700)]
+    want = [by_steps(c, 2, 0, "anchor") for c in cs]
+    torch.cuda.synchronize()
+    right = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            right.extend([torch.equal(by_steps(cs[i], 2, 0, "anchor"), want[i]) for _ in range(10)])
+    threads = [threading.Thread(target=work, args=(i % 2,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert right == [True] * 40
