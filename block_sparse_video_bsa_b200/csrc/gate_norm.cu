@@ -16,10 +16,12 @@
 // through a ring of shared-memory stages with bulk copies, and several groups
 // of warps each take the next row, so that the loads in flight do not depend on
 // registers and one group's reductions hide behind another's work (37,740 x
-// 7,168 bf16, layer and RMS norm: 372 us, 5.8 TB/s; a CTA a row takes 650 us).
-// Short rows come several a stage.  gate_norm_kernel for the rest: one CTA a
+// 7,168 bf16, layer and RMS norm: 365 to 399 us, 5.4 to 5.9 TB/s; a CTA a row
+// takes 650 us; RMS norm to codes 223 us, 3.6 TB/s, where the folded vectors
+// from shared memory and two reductions a row are most of the work for three
+// bytes a value).  Short rows come several a stage.  gate_norm_kernel for the rest: one CTA a
 // row, the row in registers between its sums, the vectors from L1 / L2; odd
-// rows in shifted chunks (20,000 x 3,971: 278 us, 2.3 TB/s; value by value
+// rows in shifted chunks (20,000 x 3,971: 280 us, 2.3 TB/s; value by value
 // 850).
 #include <type_traits>
 
@@ -632,7 +634,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) gate_norm_ring_kernel(const G
         for (int k = 0; k < 2; ++k) {
           // the codes of rows.cuh (code_bits), the products two at a time; a packed sum
           // was contracted with them into one rounding (20 of 20,000 rows of 7,168 had
-          // another code; 2 % of the time)
+          // another code; 2 % of the time).  The products and sums with gate, scale and
+          // shift above keep their two roundings: the tests hold them to that
           const float2 u = mul2(h[c].p[2 * k], pair(inv)), v = mul2(h[c].p[2 * k + 1], pair(inv));
           const uint32_t lo = __byte_perm(code_of(u.x), code_of(u.y), 0x0040);
           const uint32_t hi = __byte_perm(code_of(v.x), code_of(v.y), 0x0040);

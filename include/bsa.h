@@ -512,10 +512,15 @@ int bsa_forward_extra(const bsa_params* p, int32_t n_extra, const void* Q, const
  * contiguous.  Sums, norms and angles are fp32 or wider, and every output is
  * rounded once, to nearest even.  Outputs do not overlap inputs or each other
  * except where an entry says that it works in place (an overlap of the large
- * operands is BSA_ERR_INVALID).  Calls are deterministic, keep no state and
+ * operands is BSA_ERR_INVALID; rows that interleave in one buffer overlap only
+ * where they share bytes).  Calls are deterministic, keep no state and
  * can be captured into CUDA graphs.  A call's kernel may become resident while
  * the kernel before it on the stream still runs; it touches no memory before
- * that one is done. */
+ * that one is done.
+ * The same call gives the same bits.  A row among more or fewer rows, or rows
+ * that lie otherwise, may go through another kernel, whose sums of a norm are
+ * ordered otherwise: its values agree to fp32 rounding, and a value that near to
+ * the border of two int8 codes may have either. */
 
 typedef enum {
   BSA_DTYPE_BF16 = 0,
@@ -572,7 +577,7 @@ typedef struct {
  * 2] in radians; angles are kept as fixed-point turns, so far positions lose
  * nothing.  inverse takes no weights.
  * Q may be q itself with the same strides and type (in place), K and V
- * likewise.  Bases and strides are multiples of 16 bytes.
+ * likewise; no other tensor's rows lie there then.  Bases and strides are multiples of 16 bytes.
  * Token-major projections [B, N, 3, H, 128] to head-major [B, H, N, 128] are
  * one call: one read and one write of every row. */
 int bsa_rotary(const bsa_rotary_params* p, const void* q, const void* k, const void* v,
@@ -625,7 +630,7 @@ typedef struct {
  * not looked at.  h is written when non-NULL (it needs y),
  * z when non-NULL.  z_dtype int8: codes and z_scale [B N] as
  * bsa_quantize_int8 makes them; z_scale is NULL otherwise.  h may be x with
- * the same strides (in place). */
+ * the same strides (in place); h and z lie apart from the vectors too. */
 int bsa_gate_norm(const bsa_gate_norm_params* p, const bsa_gate_norm_inputs* in, void* h, void* z,
                   float* z_scale, void* stream);
 
@@ -697,7 +702,9 @@ size_t bsa_forward_block_workspace_bytes(const bsa_params* p, const bsa_block_pa
  *   O = bsa_forward(p, Q, K, V)
  *   y = int8(O) w_out^T + b_out         bf16                bsa_quantize_int8, bsa_linear_int8
  *   out = residual_scale x + branch_scale gate post(y)      bsa_gate_norm
- * in order on `stream`; each step as its own entry says.  out may be x. */
+ * in order on `stream`; each step as its own entry says.  out may be x; it and
+ * the workspace lie apart from the weights, vectors and positions.  The
+ * attention is bsa_forward: for its other forms call the steps one by one. */
 int bsa_forward_block(const bsa_params* p, const bsa_block_params* bp, const bsa_block_weights* w,
                       const void* x, void* out, void* workspace, size_t workspace_bytes,
                       void* stream);
