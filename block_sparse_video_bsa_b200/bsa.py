@@ -740,7 +740,8 @@ def rotary(q, k, v, positions, freqs, layout="half", axis_pairs=None, q_weight=N
                           scale, inverse, out, out_dtype)
     Q, K, V = [y if w is None or y is not None else host.empty(*w, freqs)
                for w, y in zip(want, outs)]
-    rc = host.call(lib().addresses[name], p, q, k, v, positions, freqs, q_weight, k_weight, Q, K, V,
+    rc = host.call(lib().addresses[name], p, q, k, v, positions, freqs,
+                   q_weight if q is not None else None, k_weight if k is not None else None, Q, K, V,
                    _raw_stream(device))
     if rc:
         raise BsaError(rc, name)

@@ -594,3 +594,13 @@ def test_host_calls_get_a_tensor_of_its_own():
     y = x._lazy_clone()
     assert bsa._load_host().call(ctypes.cast(record, ctypes.c_void_p).value, y, None, None, None, None) == 0
     assert seen[0] == y.data_ptr() != x.data_ptr() and seen[1:] == [None] * 4
+
+
+def test_rotary_weights_of_absent_tensors_are_not_looked_at(launches):
+    pos, freqs, w = torch.zeros(3, dtype=torch.int32), torch.ones(64, dtype=torch.float64), torch.ones(128)
+    q, k = torch.zeros(1, 4, 3, 128), torch.zeros(1, 2, 3, 128)
+    for given in ((q, None, None), (None, k, None), (None, None, k), (q, None, k), (None, k, q)):
+        bsa.rotary(*given, pos, freqs, q_weight=w, k_weight=w)
+        args = launches[-1][2]
+        assert [a is not None for a in args[:3]] == [t is not None for t in given]
+        assert [a is not None for a in args[5:7]] == [t is not None for t in given[:2]]
