@@ -71,37 +71,44 @@ struct Rows {
         range(range_of(base, size, row, n0, s0, n1, s1, n2, s2)) {}
 };
 
-// Some row of `bytes`, `at` bytes past one of the same shape, meets one of these
-// rows: strides in bytes, the largest last, each at least what the smaller ones
-// reach, so of every dimension only the two steps around `at` can come near.
-bool rows_meet(int64_t at, int64_t bytes, const int64_t* n, const int64_t* s, int dims) {
-  if (dims == 0) return at < bytes && -at < bytes;
-  const int64_t step = s[dims - 1], most = n[dims - 1] - 1;
-  if (most == 0) return rows_meet(at, bytes, n, s, dims - 1);
-  const int64_t k0 = at / step - (at % step < 0);
+// Rows a + i s of wa bytes (i below na in each dimension) and b + j s of wb (j
+// below nb), b `at` bytes past a: some share a byte.  Strides in bytes, the
+// largest last, each at least what the smaller ones reach, so of every dimension
+// only the two steps around `at` can bring them together.
+struct Steps {
+  int64_t s, na, nb;
+};
+bool rows_meet(int64_t at, int64_t wa, int64_t wb, const Steps* d, int dims) {
+  if (dims == 0) return at < wa && -at < wb;
+  const Steps& t = d[dims - 1];
+  if (t.na == 1 && t.nb == 1) return rows_meet(at, wa, wb, d, dims - 1);
+  const int64_t k0 = at / t.s - (at % t.s < 0);
   for (int64_t k = k0; k <= k0 + 1; ++k)
-    if (k <= most && -k <= most && rows_meet(at - k * step, bytes, n, s, dims - 1)) return true;
+    if (k < t.na && -k < t.nb && rows_meet(at - k * t.s, wa, wb, d, dims - 1)) return true;
   return false;
 }
 
-// No byte belongs to both: their ranges lie apart, or they are rows of one shape
-// that interleave (views of one buffer).
+// No byte belongs to both: their ranges lie apart, or they are rows at the same
+// strides that interleave (views of one buffer).
 bool apart(const Rows& a, const Rows& b) {
   if (!meet(a.range, b.range)) return true;
-  bool same = a.size == b.size && a.row == b.row;
-  for (int i = 0; i < 3; ++i)
-    same = same && a.n[i] == b.n[i] && (a.n[i] == 1 || a.s[i] == b.s[i]);
-  if (!same || !disjoint(a.row, a.n[0], a.s[0], a.n[1], a.s[1], a.n[2], a.s[2])) return false;
-  int64_t n[3], s[3];
-  int order[3] = {0, 1, 2};
+  Steps d[3];
+  int64_t n[3];
+  for (int i = 0; i < 3; ++i) {
+    const int64_t sa = a.s[i] * a.size, sb = b.s[i] * b.size;
+    if (a.n[i] > 1 && b.n[i] > 1 && sa != sb) return false;
+    d[i] = Steps{a.n[i] > 1 ? sa : sb, a.n[i], b.n[i]};
+  }
   for (int i = 0; i < 2; ++i)
     for (int j = i + 1; j < 3; ++j)
-      if (a.s[order[j]] < a.s[order[i]]) {
-        const int t = order[i];
-        order[i] = order[j], order[j] = t;
+      if (d[j].s < d[i].s) {
+        const Steps t = d[i];
+        d[i] = d[j], d[j] = t;
       }
-  for (int i = 0; i < 3; ++i) n[i] = a.n[order[i]], s[i] = a.s[order[i]] * a.size;
-  return !rows_meet(static_cast<int64_t>(b.range.lo - a.range.lo), a.row * a.size, n, s, 3);
+  for (int i = 0; i < 3; ++i) n[i] = d[i].na > d[i].nb ? d[i].na : d[i].nb;
+  const int64_t wa = a.row * a.size, wb = b.row * b.size;
+  if (!disjoint(wa > wb ? wa : wb, n[0], d[0].s, n[1], d[1].s, n[2], d[2].s)) return false;
+  return !rows_meet(static_cast<int64_t>(b.range.lo - a.range.lo), wa, wb, d, 3);
 }
 
 // Each entry checks its arguments and, with `launch`, enqueues its kernel: a

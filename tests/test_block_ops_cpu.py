@@ -604,3 +604,28 @@ def test_rotary_weights_of_absent_tensors_are_not_looked_at(launches):
         args = launches[-1][2]
         assert [a is not None for a in args[:3]] == [t is not None for t in given]
         assert [a is not None for a in args[5:7]] == [t is not None for t in given[:2]]
+
+
+@checks_alone
+def test_rotary_overlap_check_of_other_head_counts_and_types():
+    # as above with rows of several layouts: k has heads of its own, and rows of 256 or 512 bytes
+    g, met = np.random.default_rng(4), 0
+    for _ in range(600):
+        wide = int(g.integers(0, 2))
+        n = [int(g.integers(1, 4)) for _ in range(3)]
+        heads = int(g.integers(1, 5))
+        order, s, reach = g.permutation(3), [0, 0, 0], 256
+        for i in order:
+            s[i] = reach + 16 * int(g.integers(0, 60))
+            reach += (max(n[i], heads if i == 1 else 0) - 1) * s[i]
+        starts = lambda h: np.array([2 * (b * s[0] + i * s[1] + t * s[2]) for b in range(n[0]) for i in range(h) for t in range(n[2])])  # noqa: E731
+        off = 16 * int(g.integers(-reach // 8 - 2, reach // 8 + 3))
+        d = starts(heads)[:, None] + off - starts(n[1])[None]
+        want = bool(((d < 256) & (-d < 256 * (1 + wide))).any())
+        st = dict(in_b=s[0], in_h=s[1], in_n=s[2], out_b=s[0], out_h=s[1], out_n=s[2])
+        half = [x // 2 for x in s] if wide else s
+        k = dict(H=heads, in_dtype=wide, in_b=half[0], in_h=half[1], in_n=half[2], out_b=s[0], out_h=s[1], out_n=s[2])
+        got = _rot_each(dict(q=A, Q=A, k=A + off, K=A + 4 * BIG, v=None, V=None), own=dict(q=dict(H=n[1]), k=k), B=n[0], N=n[2], **st)
+        assert got == (bsa.BSA_ERR_INVALID if want else bsa.BSA_ERR_CUDA), (n, heads, s, off, wide)
+        met += want
+    assert 0 < met < 600
