@@ -897,3 +897,30 @@ def test_calls_from_two_threads(cuda_dev):
     for t in threads:
         t.join()
     assert right == [True] * 40
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_rotary_of_several_layouts_in_one_call(cuda_dev, norm):
+    # grouped heads of one packed projection, other types, one of the three in place: the bits of a call for each
+    B, N, H, G = 2, 75, 6, 2
+    buf = rnd(890, B, N, H + 2 * G, 128, dtype=torch.bfloat16)
+    q, k = buf[:, :, :H].transpose(1, 2), buf[:, :, H:H + G].transpose(1, 2)
+    v = rnd(891, B, G, N, 128)
+    pos = torch.arange(N, dtype=torch.int32, device="cuda") * 977
+    freqs, m = bsa.rotary_freqs(40)
+    wq, wk = (1 + rnd(892 + i, 128, scale=0.1) if norm else None for i in range(2))
+    kw = dict(layout="interleaved", eps=1e-5, scale=m)
+    want = (bsa.rotary(q, None, None, pos, freqs, q_weight=wq, **kw)[0], bsa.rotary(None, k, None, pos, freqs, k_weight=wk, **kw)[1], v.clone())
+    check_rotary(want[1], k, pos[None, :, None], freqs, "interleaved", [40], wk, 1e-5, m)
+    got = bsa.rotary(q, k, v, pos, freqs, q_weight=wq, k_weight=wk, **kw)
+    for a, b in zip(got, want):
+        assert a.dtype == b.dtype and torch.equal(a, b)
+    K = torch.empty(B, G, N, 128, device="cuda")
+    rest = buf[:, :, H:].clone()
+    got = bsa.rotary(q, k, v, pos, freqs, q_weight=wq, k_weight=wk, out=(q, K, v), **kw)      # in place: q and v
+    assert torch.equal(q, want[0]) and torch.equal(K.bfloat16(), want[1]) and torch.equal(v, want[2])
+    assert torch.equal(buf[:, :, H:], rest)
+    keep = buf.clone()
+    with pytest.raises(bsa.BsaError):      # k's output over q's rows, which another launch turns
+        bsa.rotary(q, k, v, pos, freqs, out=(None, buf[:, :, :G].transpose(1, 2), None), **kw)
+    assert torch.equal(buf, keep)
