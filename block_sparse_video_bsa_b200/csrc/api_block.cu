@@ -96,8 +96,9 @@ bool apart(const Rows& a, const Rows& b) {
   int64_t n[3];
   for (int i = 0; i < 3; ++i) {
     const int64_t sa = a.s[i] * a.size, sb = b.s[i] * b.size;
-    if (a.n[i] > 1 && b.n[i] > 1 && sa != sb) return false;
-    d[i] = Steps{a.n[i] > 1 ? sa : sb, a.n[i], b.n[i]};
+    const int64_t na = sa ? a.n[i] : 1, nb = sb ? b.n[i] : 1;   // a shared row is one row
+    if (na > 1 && nb > 1 && sa != sb) return false;
+    d[i] = Steps{na > 1 ? sa : sb, na, nb};
   }
   for (int i = 0; i < 2; ++i)
     for (int j = i + 1; j < 3; ++j)

@@ -629,3 +629,13 @@ def test_rotary_overlap_check_of_other_head_counts_and_types():
         assert got == (bsa.BSA_ERR_INVALID if want else bsa.BSA_ERR_CUDA), (n, heads, s, off, wide)
         met += want
     assert 0 < met < 600
+
+
+@checks_alone
+def test_gate_norm_takes_vectors_beside_its_rows():
+    # [B, 1 + N, C]: the first row of an entry is its gate, the rest are its rows, updated in place; and one vector before all rows
+    rows = dict({n + "_b": 11 * 256 for n in "xh"}, x_n=256, h_n=256, scale_b=0, shift_b=0)
+    assert _gn(dict(x=A + 512, gate=A, scale=A, shift=A), h=A + 512, mod_dtype=0, gate_b=11 * 256, **rows) == bsa.BSA_ERR_CUDA
+    assert _gn(dict(x=A + 512, gate=A), h=A + 512, mod_dtype=0, gate_b=0, **rows) == bsa.BSA_ERR_CUDA
+    assert _gn(dict(x=A + 512, gate=A + 2), h=A + 512, mod_dtype=0, gate_b=11 * 256, **rows) == bsa.BSA_ERR_INVALID
+    assert _gn(dict(x=A + 512, gate=A), h=A + 512, mod_dtype=0, gate_b=12 * 256, **rows) == bsa.BSA_ERR_INVALID
