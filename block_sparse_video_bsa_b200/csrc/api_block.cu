@@ -694,11 +694,12 @@ int bsa_forward_block(const bsa_params* p, const bsa_block_params* bp, const bsa
               {w->q_weight, 4, 128, 1, 0, 1, 0},
               {w->k_weight, 4, 128, 1, 0, 1, 0},
               {w->freqs, 8, bp->rotary_dim / 2, 1, 0, 1, 0}};
-  const Range res = range_of(out, sx, bp->C, rows, bp->C);
+  const Rows taken[2] = {Rows(workspace, 1, static_cast<int64_t>(ws.hi - ws.lo), 1, 0, 1, 0),
+                         Rows(out, sx, rows * bp->C, 1, 0, 1, 0)};
   for (const auto& r : read) {
     if (!r.base) continue;
-    const Range in = range_of(r.base, r.size, r.row, r.n0, r.s0, r.n1, r.s1);
-    if (meet(ws, in) || meet(res, in)) return BSA_ERR_INVALID;
+    const Rows in(r.base, r.size, r.row, r.n0, r.s0, r.n1, r.s1);
+    if (!apart(taken[0], in) || !apart(taken[1], in)) return BSA_ERR_INVALID;
   }
   BlockWs b;
   block_carve(p, bp->C, static_cast<uint8_t*>(workspace), &b);

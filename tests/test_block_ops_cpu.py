@@ -639,3 +639,15 @@ def test_gate_norm_takes_vectors_beside_its_rows():
     assert _gn(dict(x=A + 512, gate=A), h=A + 512, mod_dtype=0, gate_b=0, **rows) == bsa.BSA_ERR_CUDA
     assert _gn(dict(x=A + 512, gate=A + 2), h=A + 512, mod_dtype=0, gate_b=11 * 256, **rows) == bsa.BSA_ERR_INVALID
     assert _gn(dict(x=A + 512, gate=A), h=A + 512, mod_dtype=0, gate_b=12 * 256, **rows) == bsa.BSA_ERR_INVALID
+
+
+@checks_alone
+def test_forward_block_workspace_between_rows_that_are_read():
+    # one arena: an entry's gate, then the workspace, then the next entry's gate
+    p, bp = bsa.params(2, 2, 1000, 3), bsa.bsa_block_params(C=256)
+    n = bsa.lib().bsa_forward_block_workspace_bytes(ctypes.byref(p), ctypes.byref(bp))
+    ws = A + 8 * BIG
+    for gap in (1024, 1020, 256):                                # the gate's 256 values fit in the first gap alone
+        gate_b = (gap + n) // 4 + 256
+        rc = _block(ptr=dict(gate=ws - gap), gate_b=gate_b, p=p, ws=ws)
+        assert rc == (bsa.BSA_ERR_CUDA if gap == 1024 else bsa.BSA_ERR_INVALID)
